@@ -83,7 +83,8 @@ enum {
 enum {
     SPEC_STATUS_TOKEN = 1,   /* a draft or node token outside [0, V)                     */
     SPEC_STATUS_TREE = 2,    /* parents[0] != -1, parents[i] not in [0, i), or a node
-                                deeper than max_depth                                    */
+                                deeper than max_depth; spec_reorder_beams: a parent that
+                                is no beam; spec_commit_path: a malformed path          */
     SPEC_STATUS_LOGIT = 4,   /* a NaN logit, or a row with no finite normaliser
                                 (+inf present, or every entry -inf)                      */
     SPEC_STATUS_TIMEOUT = 8, /* spec_verify_linear: a warp gave up waiting (about a
@@ -93,7 +94,8 @@ enum {
                                 resident at once, else SPEC_ECUDA), so this is not
                                 expected; spec_verify_debug_wait_expiry provokes it.    */
     SPEC_STATUS_CAPACITY = 16 /* spec_plug_tokens: a sequence buffer without room for
-                                the tokens to append (or a negative length)             */
+                                the tokens to append (or a negative length); the cache
+                                calls: a length or window outside the capacity          */
 };
 
 /* Limits checked on the host. */
@@ -309,6 +311,175 @@ SPECVERIFY_API int spec_plug_tokens(const int32_t *in_tokens, const int32_t *out
                                     const int32_t *accepted_len, int batch, int k,
                                     int32_t *next_tokens, int32_t *seq_tokens, int32_t *seq_len,
                                     int capacity, int32_t *status, cudaStream_t stream);
+
+/*
+ * Beam selection: the best continuations over (beam, vocabulary).
+ * ("Accelerating Sonar through speculation", section "EAGLE": a draft tree
+ * takes the top-K candidates of its nodes, and sequences are scored; one call
+ * per level grows such a tree, and one call per step is a beam search.)
+ *   logits   [B][W][row_stride]: row w is the distribution after beam w.
+ *   scores   [B][W] fp32: the beams' sums of log probabilities; a beam with
+ *            -inf is not in use and its row is not read.
+ *   finished [B][W] int32 (nullable): a beam with a nonzero entry has ended;
+ *            its row is not read and it has the one candidate
+ *            (w, end_token) with its score unchanged.  NULL when
+ *            end_token is -1.
+ * The candidate (w, v) of another beam has the score
+ *   scores[w] + (l[v] - m)/T - ln sum_u exp((l[u] - m)/T)   (row w; m its max).
+ * The `keep` best candidates are written in order of their scores as exact
+ * numbers (they are compared to within fp64 rounding; the fp32 out_scores are
+ * rounded afterwards), equal scores by the lower w, then the lower v.  A
+ * candidate with -inf is none; slots left over get parent and token -1 and
+ * score -inf.  A row of nothing but -inf has no candidate (no error).
+ * Outputs: out_scores [B][keep] fp32, out_parents [B][keep] (w),
+ *          out_tokens [B][keep] (v), out_finished [B][keep] int32 (nullable:
+ *          1 where the token is end_token, else 0).  out_scores may be
+ *          scores, and out_finished finished, when keep == W.
+ * A request with a NaN or +inf logit in a row it reads, or a NaN or +inf
+ * score, gets parents and tokens -1, scores -inf and SPEC_STATUS_LOGIT.
+ * 1 <= W, keep <= SPEC_MAX_BEAMS; end_token in [-1, V); log2(e)/T within fp32.
+ * workspace: at least spec_beam_workspace_size(B, W, V) bytes, 256-byte
+ * aligned, not shared by calls that may overlap.
+ */
+#define SPEC_MAX_BEAMS 64
+SPECVERIFY_API size_t spec_beam_workspace_size(int batch, int beams, int vocab);
+SPECVERIFY_API int spec_beam_select(const void *logits, spec_dtype_t dtype, int64_t row_stride,
+                                    const float *scores, const int32_t *finished, int end_token,
+                                    int batch, int beams, int vocab, float temperature, int keep,
+                                    float *out_scores, int32_t *out_parents, int32_t *out_tokens,
+                                    int32_t *out_finished, int32_t *status, void *workspace,
+                                    size_t workspace_bytes, cudaStream_t stream);
+
+/*
+ * The states of the beams follow their parents, in place:
+ *   state[b][j] <- state[b][parents[b][j]]   (j < width, all at once).
+ *   states       HOST array of num_states device pointers (the keys and
+ *                values of every layer, say), all of one layout, which do
+ *                not overlap; it is read before the call returns.
+ * A state is bytes: request b's beam j starts at b * request_stride +
+ * j * beam_stride and has `segments` segments, segment_stride apart, of
+ * `capacity` units of unit_bytes each (a cache [B][W][H][T][D]: H segments
+ * of T units of D elements; [B][W][T][H][D]: one segment of T units).
+ *   begin, end   [B] int32 (nullable: 0, capacity): only units
+ *                [begin[b], end[b]) move (a prompt that all beams share
+ *                need not).  0 <= begin <= end <= capacity, else the request
+ *                is left as it was and SPEC_STATUS_CAPACITY set.
+ *   parents      [B][width] int32: -1 leaves beam j as it was; an entry
+ *                outside [-1, beams) leaves the request as it was and sets
+ *                SPEC_STATUS_TREE.
+ * Beams that are their own parent are neither read (unless another follows
+ * them) nor written.  1 <= width <= beams <= SPEC_MAX_BEAMS,
+ * 0 <= num_states <= SPEC_MAX_STATES.  Strides are at least what they step
+ * over.  Any alignment works; pointers, strides and unit_bytes that are
+ * multiples of 16 move fastest.  No workspace.
+ */
+#define SPEC_MAX_STATES 128
+SPECVERIFY_API int spec_reorder_beams(void *const *states, int num_states, int64_t request_stride,
+                                      int64_t beam_stride, int segments, int64_t segment_stride,
+                                      int64_t unit_bytes, int capacity, const int32_t *begin,
+                                      const int32_t *end, const int32_t *parents, int batch,
+                                      int beams, int width, int32_t *status, cudaStream_t stream);
+
+/*
+ * The rows of an accepted tree path move together, in place ("Accelerating
+ * Sonar through speculation", section "EAGLE": the longest acceptable
+ * sequence is kept).  The forward over the tree left node i's row at unit
+ * base[b] + i of every segment; the call moves
+ *   unit base[b] + i <- unit base[b] + path[b][i]   while path[b][i] >= 0
+ * so that the kept rows are consecutive.  States, segments and units are as
+ * in spec_reorder_beams, without beams.  The queries' rows
+ * ([B][N][heads * D], base 0) can be moved by the same call form.
+ *   path     [B][width] int32: node at depth 0, 1, ..., then -1
+ *            (spec_verify_tree's out_path_nodes, width = max_depth + 1).
+ *            Entries before the first -1 rise and stay below num_nodes; else
+ *            the request is left as it was and SPEC_STATUS_TREE set.
+ *   base     [B] int32 (nullable: 0): 0 <= base, base + num_nodes <= capacity,
+ *            else the request is left as it was and SPEC_STATUS_CAPACITY set.
+ *   out_lens [B] int32 (nullable; not base): base + the path's nodes, which
+ *            is base for a request that was left as it was.
+ * 1 <= width, num_nodes <= SPEC_MAX_NODES.
+ */
+SPECVERIFY_API int spec_commit_path(void *const *states, int num_states, int64_t request_stride,
+                                    int segments, int64_t segment_stride, int64_t unit_bytes,
+                                    int capacity, const int32_t *base, const int32_t *path,
+                                    int batch, int num_nodes, int width, int32_t *out_lens,
+                                    int32_t *status, cudaStream_t stream);
+
+/*
+ * The attention weight that a step's queries give the slots of a cache, added
+ * up: the statistic by which spec_cache_evict chooses.
+ *   q  query i of request b, head x: D elements from
+ *      b * q_request_stride + i * q_token_stride + x * q_head_stride.
+ *   k  slot t of request b, key head h: D elements from
+ *      b * k_request_stride + h * k_head_stride + t * k_slot_stride.
+ *      Strides are in elements, multiples of 16 bytes; bases are 16-byte
+ *      aligned.  Heads x = h * G + g, g < G = q_heads / kv_heads, read head h.
+ *   begin, end [B] int32: the request's filled slots before and after the
+ *      step.  Its queries are i < end - begin <= Q; query i sits at slot
+ *      begin + i and sees slots 0 .. begin + i.  (0 queries add nothing.)
+ *   out_scores[b][h][t] = (t < begin ? scores[b][h][t] : 0)
+ *      + sum_{i, g} softmax_t(scale * q_{i, hG+g} . k_{h, t})   for t < end;
+ *      scores and out_scores are [B][kv_heads][capacity] fp32 and may be the
+ *      same.  Slots from `end` on are neither read nor written.
+ * 0 <= begin <= end <= capacity and end - begin <= Q, else the request is
+ * left as it was and SPEC_STATUS_CAPACITY set.  A query whose products hold a
+ * NaN or +inf gives NaN weights.  8 <= D <= SPEC_MAX_HEAD_DIM, a multiple of
+ * 16 bytes; Q * G <= 65535; scale finite.
+ * workspace: at least spec_score_workspace_size(...) bytes, 256-byte aligned,
+ * not shared by calls that may overlap.
+ */
+#define SPEC_MAX_HEAD_DIM 256
+SPECVERIFY_API size_t spec_score_workspace_size(int batch, int queries, int q_heads, int kv_heads,
+                                                int capacity);
+SPECVERIFY_API int spec_cache_score(const void *q, const void *k, spec_dtype_t dtype,
+                                    int64_t q_request_stride, int64_t q_token_stride,
+                                    int64_t q_head_stride, int64_t k_request_stride,
+                                    int64_t k_head_stride, int64_t k_slot_stride,
+                                    const int32_t *begin, const int32_t *end, int batch,
+                                    int queries, int q_heads, int kv_heads, int head_dim,
+                                    int capacity, float scale, const float *scores,
+                                    float *out_scores, int32_t *status, void *workspace,
+                                    size_t workspace_bytes, cudaStream_t stream);
+
+/*
+ * Eviction: a cache that has grown past `budget` slots gives up those of
+ * the least accumulated attention weight, in every head by itself.
+ *   k, v       slot t of request b, head h: row_bytes bytes from
+ *              b * request_stride + h * head_stride + t * slot_stride (bytes;
+ *              k and v have their own; v may be NULL).  In place.
+ *   scores, positions [B][H][capacity] fp32, int32: a slot's accumulated
+ *              weight and the token position it holds.
+ *   lens       [B] int32: filled slots n.
+ * With n <= budget all slots stay.  Else the `budget` best stay: first those
+ * with position < sinks or position > newest - recent (newest: the head's
+ * largest position), then by the higher score, then by the lower slot; a NaN
+ * score ranks below all others and sets SPEC_STATUS_LOGIT.  Slots below
+ * `budget` that stay keep their place; the i-th slot from `budget` on that
+ * stays moves (k, v, score, position) to the i-th place below that was given
+ * up.  So slots are not in order of position afterwards, few rows move, and
+ * rows from `budget` on are left as they were.
+ * Outputs: out_scores, out_positions [B][H][capacity]: slots
+ *          [0, min(n, budget)) are written; each may be its input, and
+ *          overlaps it in no other way;
+ *          out_lens [B] = min(n, budget); may be lens.
+ * A request with n outside [0, capacity] is left as it was, with
+ * SPEC_STATUS_CAPACITY set and out_lens = n.
+ * sinks, recent >= 0; sinks + recent <= budget; 1 <= budget; capacity <=
+ * SPEC_MAX_SLOTS.  Any alignment works; 16-byte multiples move fastest.
+ * workspace: at least spec_evict_workspace_size(B, H, capacity, budget)
+ * bytes, 256-byte aligned, not shared by calls that may overlap.
+ */
+#define SPEC_MAX_SLOTS 262144
+SPECVERIFY_API size_t spec_evict_workspace_size(int batch, int heads, int capacity, int budget);
+SPECVERIFY_API int spec_cache_evict(void *k, void *v, int64_t k_request_stride, int64_t k_head_stride,
+                                    int64_t k_slot_stride, int64_t k_row_bytes,
+                                    int64_t v_request_stride, int64_t v_head_stride,
+                                    int64_t v_slot_stride, int64_t v_row_bytes, const float *scores,
+                                    const int32_t *positions, const int32_t *lens, int batch,
+                                    int heads, int capacity, int budget, int sinks, int recent,
+                                    float *out_scores, int32_t *out_positions, int32_t *out_lens,
+                                    int32_t *status, void *workspace, size_t workspace_bytes,
+                                    cudaStream_t stream);
 
 /*
  * Vocabulary-sharded verification ("Accelerating Sonar through speculation",

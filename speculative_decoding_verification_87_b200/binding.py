@@ -8,6 +8,7 @@ is no fallback.  If the library has not been built, the first call raises.
 
 Build it with ``python -m speculative_decoding_verification_87_b200.build``.
 """
+import contextlib
 import ctypes
 import os
 import threading
@@ -21,12 +22,16 @@ SPEC_F32, SPEC_BF16 = 0, 1
 SPEC_OK = 0
 STATUS_TOKEN, STATUS_TREE, STATUS_LOGIT, STATUS_TIMEOUT, STATUS_CAPACITY = 1, 2, 4, 8, 16
 MAX_K, MAX_NODES = 32, 1024
+MAX_BEAMS, MAX_STATES, MAX_HEAD_DIM, MAX_SLOTS = 64, 128, 256, 262144
 SYMBOLS = ("spec_verify_workspace_size", "spec_verify_strerror", "spec_verify_linear",
            "spec_verify_greedy", "spec_verify_tree", "spec_verify_debug_uniforms",
            "spec_verify_linear_noalloc", "spec_verify_debug_exp2", "spec_verify_greedy_walk",
            "spec_verify_tree_greedy_walk", "spec_verify_debug_wait_expiry", "spec_plug_tokens",
            "spec_shard_row_stats", "spec_shard_decide", "spec_shard_decide_greedy",
-           "spec_shard_draw_sums", "spec_shard_draw_pick", "spec_shard_emit")
+           "spec_shard_draw_sums", "spec_shard_draw_pick", "spec_shard_emit",
+           "spec_beam_workspace_size", "spec_beam_select", "spec_reorder_beams",
+           "spec_commit_path", "spec_score_workspace_size", "spec_cache_score",
+           "spec_evict_workspace_size", "spec_cache_evict")
 NOALLOC_SCRATCH_BYTES = 8 << 20
 
 _lib = None
@@ -97,6 +102,27 @@ def load_library(path: str = LIB_PATH):
         L.spec_shard_draw_pick.restype = _I
         L.spec_shard_emit.argtypes = [_P, _P, _I, _I, _P, _P]
         L.spec_shard_emit.restype = _I
+        L.spec_beam_workspace_size.argtypes = [_I, _I, _I]
+        L.spec_beam_workspace_size.restype = _SZ
+        L.spec_beam_select.argtypes = [_P, _I, _I64, _P, _P, _I, _I, _I, _I, _F, _I, _P, _P, _P, _P,
+                                       _P, _P, _SZ, _P]
+        L.spec_beam_select.restype = _I
+        L.spec_reorder_beams.argtypes = [_P, _I, _I64, _I64, _I, _I64, _I64, _I, _P, _P, _P, _I, _I,
+                                         _I, _P, _P]
+        L.spec_reorder_beams.restype = _I
+        L.spec_commit_path.argtypes = [_P, _I, _I64, _I, _I64, _I64, _I, _P, _P, _I, _I, _I, _P, _P,
+                                       _P]
+        L.spec_commit_path.restype = _I
+        L.spec_score_workspace_size.argtypes = [_I, _I, _I, _I, _I]
+        L.spec_score_workspace_size.restype = _SZ
+        L.spec_cache_score.argtypes = [_P, _P, _I, _I64, _I64, _I64, _I64, _I64, _I64, _P, _P, _I,
+                                       _I, _I, _I, _I, _I, _F, _P, _P, _P, _P, _SZ, _P]
+        L.spec_cache_score.restype = _I
+        L.spec_evict_workspace_size.argtypes = [_I, _I, _I, _I]
+        L.spec_evict_workspace_size.restype = _SZ
+        L.spec_cache_evict.argtypes = [_P, _P, _I64, _I64, _I64, _I64, _I64, _I64, _I64, _I64, _P,
+                                       _P, _P, _I, _I, _I, _I, _I, _I, _P, _P, _P, _P, _P, _SZ, _P]
+        L.spec_cache_evict.restype = _I
         _lib = L
         return L
 
@@ -430,6 +456,307 @@ def spec_plug_tokens(in_tokens, out_tokens, accepted_len, next_tokens=None, seq_
                                          _ptr(status), _stream(stream))
     _check(rc, "spec_plug_tokens")
     return next_tokens
+
+
+# ------------------------------------------------------------ beams, paths and caches
+# These calls run on the device of their tensors, whichever is current, and
+# on `stream` (a stream of that device; default: the device's current one).
+# What they allocate belongs to that stream.
+
+def _on(dev, stream):
+    """The context in which a call on `dev` runs."""
+    if stream is not None:
+        if stream.device != dev:
+            raise ValueError(f"stream is on {stream.device}, the tensors on {dev}")
+        return torch.cuda.stream(stream)
+    if dev.index == torch.cuda.current_device():
+        return contextlib.nullcontext()
+    return torch.cuda.device(dev)
+
+
+def _one_device(dev, **tensors):
+    for name, t in tensors.items():
+        if t is not None and t.device != dev:
+            raise ValueError(f"{name} is on {t.device}, not on {dev}")
+
+
+def _scratch(need, buf, dev):
+    """A workspace of `need` bytes: the caller's, or a new one (the caching
+    allocator's blocks are 512-byte aligned; a captured graph gets its own)."""
+    if buf is not None:
+        _need_cuda("workspace_buf", buf, torch.uint8)
+        return buf
+    if need == 0:
+        raise ValueError("invalid workspace request")
+    return torch.empty(need, dtype=torch.uint8, device=dev)
+
+
+def spec_beam_select(logits, scores, vocab, keep, temperature=1.0, finished=None, end_token=-1,
+                     out_scores=None, out_parents=None, out_tokens=None, out_finished=None,
+                     status=None, workspace_buf=None, stream=None):
+    """The `keep` best continuations (beam, token) of each request by summed
+    log probability.  logits [B][W][stride] (bf16/fp32), scores [B][W] fp32,
+    finished [B][W] int32 or None (an ended beam goes on as end_token with
+    its score unchanged).  Returns (scores [B][keep], parents [B][keep],
+    tokens [B][keep], finished [B][keep] or None)."""
+    _need_cuda("logits", logits)
+    B, W, stride = logits.shape
+    keep = int(keep)
+    dev = logits.device
+    _need_cuda("scores", scores, torch.float32, (B, W))
+    if finished is not None:
+        _need_cuda("finished", finished, torch.int32, (B, W))
+    with _on(dev, stream):
+        if out_scores is None:
+            out_scores = torch.empty((B, keep), dtype=torch.float32, device=dev)
+        if out_parents is None:
+            out_parents = torch.empty((B, keep), dtype=torch.int32, device=dev)
+        if out_tokens is None:
+            out_tokens = torch.empty((B, keep), dtype=torch.int32, device=dev)
+        if out_finished is None and finished is not None:
+            out_finished = torch.empty((B, keep), dtype=torch.int32, device=dev)
+        _need_cuda("out_scores", out_scores, torch.float32, (B, keep))
+        for name, t in (("out_parents", out_parents), ("out_tokens", out_tokens)):
+            _need_cuda(name, t, torch.int32, (B, keep))
+        if out_finished is not None:
+            _need_cuda("out_finished", out_finished, torch.int32, (B, keep))
+        if status is not None:
+            _need_cuda("status", status, torch.int32)
+        _one_device(dev, scores=scores, finished=finished, out_scores=out_scores,
+                    out_parents=out_parents, out_tokens=out_tokens, out_finished=out_finished,
+                    status=status, workspace_buf=workspace_buf)
+        lib = load_library()
+        code = _dtype_code(logits)
+        ws = None
+        if B > 0:
+            need = lib.spec_beam_workspace_size(B, W, vocab)
+            ws = _scratch(need, workspace_buf, dev) if need else workspace_buf
+        rc = lib.spec_beam_select(
+            _ptr(logits), code, stride, _ptr(scores), _ptr(finished), int(end_token), B, W, vocab,
+            float(temperature), keep, _ptr(out_scores), _ptr(out_parents), _ptr(out_tokens),
+            _ptr(out_finished), _ptr(status), _ptr(ws), 0 if ws is None else ws.numel(),
+            _stream(stream))
+    _check(rc, "spec_beam_select")
+    return out_scores, out_parents, out_tokens, out_finished
+
+
+def _one_stride(sizes, strides):
+    """(count, stride) of the flattened dimensions, or None if no single stride steps over them."""
+    count, step = 1, 0
+    for n, s in zip(reversed(sizes), reversed(strides)):
+        if n == 1:
+            continue
+        if count == 1:
+            step = s
+        elif s != count * step:
+            return None
+        count *= n
+    return count, step
+
+
+def _state_layout(states, lead, axis):
+    """The common layout of `states`, whose first `lead` dimensions are the
+    request (and the beam): (segments, segment stride, unit bytes, capacity)
+    and the device.  axis: the dimension of the units (positions), or None
+    where a whole state is one unit."""
+    t = states[0]
+    if t.dim() < lead or (axis is not None and not lead <= axis < t.dim()):
+        raise ValueError("axis must be a dimension after the request's and the beam's")
+    e = t.element_size()
+    shape, stride = tuple(t.shape), tuple(t.stride())
+    for i, x in enumerate(states):
+        if not x.is_cuda:
+            raise ValueError(f"states[{i}] must be a CUDA tensor")
+        if x.device != t.device or x.dtype != t.dtype or tuple(x.shape) != shape or x.stride() != stride:
+            raise ValueError("the states must share device, dtype, shape and strides")
+    inner = lead if axis is None else axis + 1
+    whole = _one_stride(shape[inner:], stride[inner:])
+    if whole is None or (whole[0] > 1 and whole[1] != 1):
+        raise ValueError("the dimensions of a unit must be contiguous")
+    unit = whole[0] * e
+    if axis is None:
+        return 1, 0, unit, 1, t.device
+    if shape[axis] > 1 and stride[axis] * e != unit:
+        raise ValueError("the units must follow one another")
+    seg = _one_stride(shape[lead:axis], stride[lead:axis])
+    if seg is None:
+        raise ValueError("the dimensions before the units must have one stride")
+    return seg[0], seg[1] * e, unit, shape[axis], t.device
+
+
+def _pointers(states):
+    return (ctypes.c_void_p * len(states))(*(t.data_ptr() for t in states))
+
+
+def spec_reorder_beams(states, parents, axis=None, begin=None, end=None, status=None, stream=None):
+    """states[s][b][j] <- states[s][b][parents[b][j]], in place.  states: a
+    list of tensors [B][W][...] of one layout (at most MAX_STATES); parents
+    [B][width] int32, width <= W (-1: left as it was).  axis: the dimension
+    of positions, of which only [begin[b], end[b]) move ([B] int32, None: the
+    first and one past the last); axis None moves whole states.  Returns
+    states."""
+    states = list(states)
+    _need_cuda("parents", parents, torch.int32)
+    if parents.dim() != 2:
+        raise ValueError("parents must be [B][width]")
+    B, width = parents.shape
+    if not states:
+        return states
+    segments, seg_stride, unit, cap, dev = _state_layout(states, 2, axis)
+    W = states[0].shape[1]
+    if states[0].shape[0] != B:
+        raise ValueError(f"parents must have {states[0].shape[0]} rows, got {B}")
+    if axis is None and (begin is not None or end is not None):
+        raise ValueError("begin and end need axis")
+    for name, t in (("begin", begin), ("end", end)):
+        if t is not None:
+            _need_cuda(name, t, torch.int32, (B,))
+    if status is not None:
+        _need_cuda("status", status, torch.int32)
+    _one_device(dev, parents=parents, begin=begin, end=end, status=status)
+    e = states[0].element_size()
+    with _on(dev, stream):
+        rc = load_library().spec_reorder_beams(
+            _pointers(states), len(states), states[0].stride(0) * e, states[0].stride(1) * e,
+            segments, seg_stride, unit, cap, _ptr(begin), _ptr(end), _ptr(parents), B, W, width,
+            _ptr(status), _stream(stream))
+    _check(rc, "spec_reorder_beams")
+    return states
+
+
+def spec_commit_path(states, base, path, num_nodes, axis, out_lens=None, status=None, stream=None):
+    """Move the rows of an accepted tree path together, in place: position
+    base[b] + i <- base[b] + path[b][i].  states: a list of tensors [B][...]
+    of one layout whose dimension `axis` holds the positions; base [B] int32
+    or None (0); path [B][width] int32 (spec_verify_tree's out_path_nodes).
+    Returns the new lengths [B] int32 (base + nodes of the path)."""
+    states = list(states)
+    _need_cuda("path", path, torch.int32)
+    if path.dim() != 2:
+        raise ValueError("path must be [B][width]")
+    B, width = path.shape
+    segments, seg_stride, unit, cap, dev = 1, 0, 1, 1 << 30, path.device
+    if states:
+        segments, seg_stride, unit, cap, dev = _state_layout(states, 1, axis)
+        if states[0].shape[0] != B:
+            raise ValueError(f"path must have {states[0].shape[0]} rows, got {B}")
+    if base is not None:
+        _need_cuda("base", base, torch.int32, (B,))
+    with _on(dev, stream):
+        if out_lens is None:
+            out_lens = torch.empty((B,), dtype=torch.int32, device=dev)
+        _need_cuda("out_lens", out_lens, torch.int32, (B,))
+        if status is not None:
+            _need_cuda("status", status, torch.int32)
+        _one_device(dev, base=base, path=path, out_lens=out_lens, status=status)
+        step = states[0].stride(0) * states[0].element_size() if states else cap
+        rc = load_library().spec_commit_path(
+            _pointers(states), len(states), step, segments, seg_stride, unit, cap, _ptr(base),
+            _ptr(path), B, int(num_nodes), width, _ptr(out_lens), _ptr(status), _stream(stream))
+    _check(rc, "spec_commit_path")
+    return out_lens
+
+
+def _inner_contiguous(name, t, dims):
+    if t is None:
+        raise ValueError(f"{name} is required")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dim() != dims:
+        raise ValueError(f"{name} must have {dims} dimensions, got {t.dim()}")
+    if t.shape[-1] > 1 and t.stride(-1) != 1:
+        raise ValueError(f"the last dimension of {name} must be contiguous")
+
+
+def spec_cache_score(q, k, begin, end, scores, scale=None, out_scores=None, status=None,
+                     workspace_buf=None, stream=None):
+    """Add the attention weight that a step's queries give a cache's slots.
+    q [B][Q][heads][D], k [B][kv_heads][capacity][D] (bf16/fp32, any strides
+    with D contiguous: a cache [B][capacity][kv_heads][D] is passed as
+    k.transpose(1, 2)); begin, end [B] int32: filled slots before and after
+    the step (query i sits at slot begin + i; end - begin <= Q);
+    scores [B][kv_heads][capacity] fp32.  scale: default D ** -0.5.  Writes
+    out_scores (default: scores, in place) below `end` and returns it."""
+    _inner_contiguous("q", q, 4)
+    _inner_contiguous("k", k, 4)
+    B, Q, Hq, D = q.shape
+    H, cap = k.shape[1], k.shape[2]
+    if k.dtype != q.dtype or tuple(k.shape) != (B, H, cap, D):
+        raise ValueError(f"k must be [{B}][kv_heads][capacity][{D}] of {q.dtype}, got {tuple(k.shape)} {k.dtype}")
+    dev = q.device
+    _need_cuda("begin", begin, torch.int32, (B,))
+    _need_cuda("end", end, torch.int32, (B,))
+    _need_cuda("scores", scores, torch.float32, (B, H, cap))
+    out_scores = scores if out_scores is None else out_scores
+    _need_cuda("out_scores", out_scores, torch.float32, (B, H, cap))
+    if status is not None:
+        _need_cuda("status", status, torch.int32)
+    _one_device(dev, k=k, begin=begin, end=end, scores=scores, out_scores=out_scores, status=status,
+                workspace_buf=workspace_buf)
+    scale = D ** -0.5 if scale is None else float(scale)
+    lib = load_library()
+    with _on(dev, stream):
+        ws = None
+        if B > 0:
+            need = lib.spec_score_workspace_size(B, Q, Hq, H, cap)
+            ws = _scratch(need, workspace_buf, dev) if need else workspace_buf
+        rc = lib.spec_cache_score(
+            _ptr(q), _ptr(k), _dtype_code(q), q.stride(0), q.stride(1), q.stride(2), k.stride(0),
+            k.stride(1), k.stride(2), _ptr(begin), _ptr(end), B, Q, Hq, H, D, cap, scale,
+            _ptr(scores), _ptr(out_scores), _ptr(status), _ptr(ws),
+            0 if ws is None else ws.numel(), _stream(stream))
+    _check(rc, "spec_cache_score")
+    return out_scores
+
+
+def spec_cache_evict(k, v, scores, positions, lens, budget, sinks=0, recent=0, out_scores=None,
+                     out_positions=None, out_lens=None, status=None, workspace_buf=None, stream=None):
+    """Cut a cache down to `budget` slots a head by accumulated attention
+    weight, k and v in place.  k, v [B][H][capacity][D] (any dtype, any
+    strides with D contiguous; v may be None), scores [B][H][capacity] fp32,
+    positions the same shape int32, lens [B] int32.  Positions < sinks and the
+    `recent` newest stay in any case.  Returns (out_scores, out_positions,
+    out_lens); the first two default to in place, out_lens to a new tensor."""
+    _inner_contiguous("k", k, 4)
+    B, H, cap, _ = k.shape
+    dev = k.device
+    if v is not None:
+        _inner_contiguous("v", v, 4)
+        if tuple(v.shape[:3]) != (B, H, cap):
+            raise ValueError(f"v must be [{B}][{H}][{cap}][D], got {tuple(v.shape)}")
+    _need_cuda("scores", scores, torch.float32, (B, H, cap))
+    _need_cuda("positions", positions, torch.int32, (B, H, cap))
+    _need_cuda("lens", lens, torch.int32, (B,))
+    out_scores = scores if out_scores is None else out_scores
+    out_positions = positions if out_positions is None else out_positions
+    _need_cuda("out_scores", out_scores, torch.float32, (B, H, cap))
+    _need_cuda("out_positions", out_positions, torch.int32, (B, H, cap))
+
+    def layout(t):
+        e = t.element_size()
+        return t.stride(0) * e, t.stride(1) * e, t.stride(2) * e, t.shape[3] * e
+
+    lib = load_library()
+    with _on(dev, stream):
+        if out_lens is None:
+            out_lens = torch.empty((B,), dtype=torch.int32, device=dev)
+        _need_cuda("out_lens", out_lens, torch.int32, (B,))
+        if status is not None:
+            _need_cuda("status", status, torch.int32)
+        _one_device(dev, v=v, scores=scores, positions=positions, lens=lens, out_scores=out_scores,
+                    out_positions=out_positions, out_lens=out_lens, status=status,
+                    workspace_buf=workspace_buf)
+        ws = None
+        if B > 0:
+            need = lib.spec_evict_workspace_size(B, H, cap, int(budget))
+            ws = _scratch(need, workspace_buf, dev) if need else workspace_buf
+        rc = lib.spec_cache_evict(
+            _ptr(k), _ptr(v), *layout(k), *(layout(v) if v is not None else (0, 0, 0, 0)),
+            _ptr(scores), _ptr(positions), _ptr(lens), B, H, cap, int(budget), int(sinks),
+            int(recent), _ptr(out_scores), _ptr(out_positions), _ptr(out_lens), _ptr(status),
+            _ptr(ws), 0 if ws is None else ws.numel(), _stream(stream))
+    _check(rc, "spec_cache_evict")
+    return out_scores, out_positions, out_lens
 
 
 # ------------------------------------------------------------ vocabulary-sharded steps

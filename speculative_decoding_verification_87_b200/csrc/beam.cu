@@ -1,0 +1,584 @@
+// beam.cu -- spec_beam_select: the best continuations over (beam, vocabulary).
+//
+// "Accelerating Sonar through speculation", section "EAGLE": a draft tree
+// takes top-K candidates and scores their sequences; one call per level
+// grows the tree that spec_verify_tree verifies.
+//
+// Mathematics.  The score of (w, v) is base_w + (l_v - m_w)/T with
+// base_w = scores_w - ln sum_u exp((l_u - m_w)/T), so
+//  (1) inside a row candidates are ordered by their logits alone, exactly;
+//  (2) a candidate among the K best lies in one of the at most K items (2048
+//      bf16 or 1024 fp32 entries of a row) whose maxima are the best: an item
+//      that comes before its own item's maximum holds a better candidate.
+// Pass 1 (k_pass1 of sv_verify.cuh) therefore reads every logit once for
+// (max, sum exp) per item, and the select step re-reads about K items per
+// request, whatever W is.
+//
+// Order.  The scores are compared as exact numbers.  Pass 1 leaves base_w
+// with an error below kBaseErr; two candidates of different rows that lie
+// within the sum of their rows' errors are told apart by recomputing those
+// rows' sums in fp64 (one block, rarely: with K = 16 about one request in a
+// thousand), after which the order holds to fp64 rounding.
+#include <algorithm>
+#include <climits>
+#include <cmath>
+#include <cstdint>
+#include <cstring>
+#include <mutex>
+
+#include <cuda_runtime.h>
+
+#include "../../include/specverify.h"
+#include "sv_common.cuh"
+#include "sv_verify.cuh"
+
+namespace sv {
+namespace {
+
+constexpr int kBeamThreads = 512;
+constexpr int kBeamWarps = kBeamThreads / 32;
+constexpr int kListMax = 256;  // items kept on the fast path
+// Bound on |ln S - ln S_exact| for a row sum merged from pass-1 partials:
+// every term carries the exponential's 2^-22 and at most |z| 2^-23 ln 2 from
+// rounding log2(e)/T and z = (l - m) log2(e)/T, whose weighted mean is at most
+// log2 V bits (entropy), 1.5e-6 for V = 2^18; the sums of an item (17
+// additions deep, 2^-24 each) and the rescaling by fp32 exponentials 1.4e-6
+// and 1.2e-6 more.
+constexpr double kBaseErr = 6e-6;
+
+struct BeamArgs {
+    int end_token, keep, cap;  // cap: candidates the shared list holds
+    float *out_s;
+    int32_t *out_p, *out_t, *out_f;
+};
+
+struct Cand {
+    double s;
+    int w, v;
+};
+
+// The documented order: score, then lower beam, then lower token.
+__device__ __forceinline__ bool better(const Cand &a, const Cand &b)
+{
+    return a.s > b.s || (a.s == b.s && (a.w < b.w || (a.w == b.w && a.v < b.v)));
+}
+
+// fp32 to an unsigned integer of the same order (and back).
+__device__ __forceinline__ uint32_t order_key(float x)
+{
+    const uint32_t u = __float_as_uint(x);
+    return (u & 0x80000000u) ? ~u : u | 0x80000000u;
+}
+__device__ __forceinline__ float order_value(uint32_t k)
+{
+    return __uint_as_float((k & 0x80000000u) ? k ^ 0x80000000u : ~k);
+}
+
+enum : int { kRowNone = 0, kRowLive = 1, kRowDone = 2 };
+
+struct BeamRows {
+    double base[SPEC_MAX_BEAMS];  // scores - ln S
+    double err[SPEC_MAX_BEAMS];   // bound on base's error
+    double s[SPEC_MAX_BEAMS];
+    float m[SPEC_MAX_BEAMS];
+    int idx[SPEC_MAX_BEAMS];      // merge_row's argmax slot (unused here)
+    float score[SPEC_MAX_BEAMS];
+    int kind[SPEC_MAX_BEAMS];
+    int exact[SPEC_MAX_BEAMS];    // 1: recompute wanted, 2: done
+};
+
+// Append the candidates of one item (row w, segment s) that reach lthr to
+// the list, at most `keep` of them: if more qualify, its `keep` best.  One
+// warp.  Returns through *count the list's new length, which may pass cap
+// (entries beyond it are not stored).
+template <class Tag>
+__device__ __forceinline__ void gather_item(const Params &p, int b, int w, int s, float lthr, double base,
+                                            float m, int keep, Cand *cand, int cap, int *count)
+{
+    constexpr int kVec = Tag::kVec;
+    constexpr int kV = Pass1Shape<Tag>::kVecL;
+    constexpr int kEsz = sizeof(typename Tag::elem);
+    const int lane = threadIdx.x & 31;
+    const int e0 = s * Pass1Shape<Tag>::kItem;
+    const char *row = static_cast<const char *>(p.tl) + (static_cast<int64_t>(b) * p.R + w) * p.stride * kEsz;
+    uint4 raw[kV];
+#pragma unroll
+    for (int v = 0; v < kV; ++v) {
+        const int e = e0 + (v * 32 + lane) * kVec;
+        raw[v] = e < p.V ? mask_tail<Tag>(ldg_vec(row + static_cast<int64_t>(e) * kEsz), p.V - e)
+                         : make_uint4(Tag::kNegInfWord, Tag::kNegInfWord, Tag::kNegInfWord, Tag::kNegInfWord);
+    }
+    auto reaching = [&](float t) {  // entries >= t above -inf
+        int c = 0;
+#pragma unroll
+        for (int v = 0; v < kV; ++v) {
+            float x[kVec];
+            unpack<Tag>(raw[v], x);
+#pragma unroll
+            for (int e = 0; e < kVec; ++e) c += (x[e] >= t && x[e] > -INFINITY) ? 1 : 0;
+        }
+        return __reduce_add_sync(kFull, c);
+    };
+    int c = reaching(lthr);
+    if (c == 0) return;
+    float t = lthr;
+    int ties = INT_MAX;  // entries equal to t to take, in index order
+    if (c > keep) {
+        // the largest t that at least `keep` entries reach
+        uint32_t lo = order_key(lthr), hi = order_key(INFINITY);
+        while (lo < hi) {
+            const uint32_t mid = lo + (hi - lo + 1) / 2;
+            if (reaching(order_value(mid)) >= keep) lo = mid;
+            else hi = mid - 1;
+        }
+        t = order_value(lo);
+        int above = 0;
+#pragma unroll
+        for (int v = 0; v < kV; ++v) {
+            float x[kVec];
+            unpack<Tag>(raw[v], x);
+#pragma unroll
+            for (int e = 0; e < kVec; ++e) above += x[e] > t ? 1 : 0;
+        }
+        ties = keep - __reduce_add_sync(kFull, above);
+        c = keep;
+    }
+    int at = 0;
+    if (lane == 0) at = atomicAdd(count, c);
+    at = __shfl_sync(kFull, at, 0);
+#pragma unroll
+    for (int v = 0; v < kV; ++v) {
+        float x[kVec];
+        unpack<Tag>(raw[v], x);
+        int eq = 0, gt = 0;
+#pragma unroll
+        for (int e = 0; e < kVec; ++e) {
+            const bool in = x[e] >= t && x[e] > -INFINITY;
+            eq += in && x[e] == t ? 1 : 0;
+            gt += in && x[e] != t ? 1 : 0;
+        }
+        if (!__any_sync(kFull, (eq | gt) != 0)) continue;
+        // lane prefixes: an equal entry is taken while `ties` lasts
+        int peq = eq, pgt = gt;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int a = __shfl_up_sync(kFull, peq, o), g = __shfl_up_sync(kFull, pgt, o);
+            if (lane >= o) {
+                peq += a;
+                pgt += g;
+            }
+        }
+        const int teq = __shfl_sync(kFull, peq, 31), tgt = __shfl_sync(kFull, pgt, 31);
+        int seen = peq - eq;                         // equal entries of lower lanes
+        int slot = at + (pgt - gt) + min(seen, ties);
+#pragma unroll
+        for (int e = 0; e < kVec; ++e) {
+            if (!(x[e] >= t && x[e] > -INFINITY)) continue;
+            if (x[e] == t && seen++ >= ties) continue;
+            if (slot < cap)
+                cand[slot] = {base + (static_cast<double>(x[e]) - static_cast<double>(m)) * p.inv_t, w,
+                              e0 + (v * 32 + lane) * kVec + e};
+            ++slot;
+        }
+        at += tgt + min(teq, ties);
+        ties -= min(teq, ties);
+    }
+}
+
+// The fp64 sum of exp((l - m)/T) over row w of request b, the same order
+// of additions for every row (equal rows give equal sums).  Whole block.
+template <class Tag>
+__device__ __forceinline__ double exact_sum(const Params &p, int b, int w, float m, const double *tab,
+                                            double *scratch)
+{
+    constexpr int kVec = Tag::kVec;
+    constexpr int kEsz = sizeof(typename Tag::elem);
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const char *row = static_cast<const char *>(p.tl) + (static_cast<int64_t>(b) * p.R + w) * p.stride * kEsz;
+    double acc = 0.0;
+    for (int e0 = tid * kVec; e0 < p.V; e0 += kBeamThreads * kVec) {
+        float x[kVec];
+        unpack<Tag>(mask_tail<Tag>(ldg_vec(row + static_cast<int64_t>(e0) * kEsz), p.V - e0), x);
+#pragma unroll
+        for (int e = 0; e < kVec; ++e)
+            acc += exp2_fp64((static_cast<double>(x[e]) - static_cast<double>(m)) * p.c64, tab);
+    }
+    acc = warp_sum(acc);
+    __syncthreads();
+    if (lane == 0) scratch[warp] = acc;
+    __syncthreads();
+    double sum = 0.0;
+    for (int i = 0; i < kBeamWarps; ++i) sum += scratch[i];
+    return sum;
+}
+
+// Select: one block per request, after pass 1.
+template <class Tag>
+__global__ void __launch_bounds__(kBeamThreads)
+    k_beam_select(const __grid_constant__ Params p, const __grid_constant__ BeamArgs a)
+{
+    extern __shared__ Cand cand[];
+    __shared__ BeamRows rw;
+    __shared__ double tab[kExp2Tab];
+    __shared__ double scratch[kBeamWarps];
+    __shared__ Cand best[SPEC_MAX_BEAMS];
+    __shared__ int list[kListMax];
+    __shared__ int nlist, ncand, bad, again;
+    __shared__ Cand warp_best[kBeamWarps];
+
+    const int b = blockIdx.x, W = p.R, S = p.S, K = a.keep;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    if (tid == 0) bad = 0;
+    __syncthreads();
+    if (tid < W) {
+        const float sc = __ldg(p.beam_scores + static_cast<int64_t>(b) * W + tid);
+        const bool done = p.beam_done && __ldg(p.beam_done + static_cast<int64_t>(b) * W + tid) != 0;
+        rw.score[tid] = sc;
+        rw.kind[tid] = sc == -INFINITY ? kRowNone : done ? kRowDone : kRowLive;
+        rw.exact[tid] = 0;
+        if (!(sc < INFINITY)) bad = 1;  // NaN or +inf
+    }
+    asm volatile("griddepcontrol.wait;\n" ::: "memory");
+    __syncthreads();
+    for (int w = warp; w < W; w += kBeamWarps)
+        if (rw.kind[w] == kRowLive) merge_row<kBeam>(p, b, w, RowStats{rw.s, rw.m, rw.idx});
+    __syncthreads();
+    if (tid < W && rw.kind[tid] == kRowLive) {
+        const float m = rw.m[tid];
+        if (m == -INFINITY) {
+            rw.kind[tid] = kRowNone;  // nothing to go on with
+        } else if (!stoch_row_ok(m, rw.s[tid])) {
+            bad = 1;
+        } else {
+            rw.base[tid] = static_cast<double>(rw.score[tid]) - log(rw.s[tid]);
+            rw.err[tid] = kBaseErr;
+        }
+    }
+    __syncthreads();
+    const int64_t o = static_cast<int64_t>(b) * K;
+    if (bad) {
+        if (tid < K) {
+            a.out_s[o + tid] = -INFINITY;
+            a.out_p[o + tid] = -1;
+            a.out_t[o + tid] = -1;
+            if (a.out_f) a.out_f[o + tid] = 0;
+        }
+        if (tid == 0) report(p.status, kStLogit);
+        return;
+    }
+
+    const float2 *part = p.rowpart + static_cast<int64_t>(b) * W * S;
+    const int items = W * S;
+    // score of item i's best candidate (-inf: none)
+    auto item_score = [&](int i) -> double {
+        const int w = i / S;
+        if (rw.kind[w] != kRowLive) return -INFINITY;
+        const float m = __ldcg(&part[i].x);
+        return m == -INFINITY ? -INFINITY
+                              : rw.base[w] + (static_cast<double>(m) - static_cast<double>(rw.m[w])) * p.inv_t;
+    };
+    int found = 0;
+    for (;;) {
+        // a lower bound t0 of the K-th best candidate: the K-th largest of
+        // the threads' item maxima (each a candidate's score)
+        float mine = -INFINITY;
+        for (int i = tid; i < items; i += kBeamThreads) mine = fmaxf(mine, static_cast<float>(item_score(i)));
+        uint32_t lo = order_key(-INFINITY), hi = order_key(INFINITY);
+        const uint32_t key = order_key(mine);
+        while (lo < hi) {
+            const uint32_t mid = lo + (hi - lo + 1) / 2;
+            if (__syncthreads_count(key >= mid) >= K) lo = mid;
+            else hi = mid - 1;
+        }
+        const float t0f = order_value(lo);
+        // below t0 by the rounding of `mine` and the rows' errors, so that
+        // what the check below compares is in the list too
+        const double t0 = t0f == -INFINITY ? -INFINITY
+                                           : static_cast<double>(t0f) - (4.0 * kBaseErr + fabs(static_cast<double>(t0f)) * 2.4e-7);
+        if (tid == 0) {
+            nlist = 0;
+            ncand = 0;
+            again = 0;
+        }
+        __syncthreads();
+        for (int i = tid; i < items; i += kBeamThreads) {
+            const double s = item_score(i);
+            if (s >= t0 && s > -INFINITY) {
+                const int at = atomicAdd(&nlist, 1);
+                if (at < kListMax) list[at] = i;
+            }
+        }
+        if (tid < W && rw.kind[tid] == kRowDone) {
+            const int at = atomicAdd(&ncand, 1);
+            cand[at] = {static_cast<double>(rw.score[tid]), tid, a.end_token};
+        }
+        __syncthreads();
+        bool whole = nlist <= kListMax;
+        auto gather = [&](int n) {
+            for (int j = warp; j < n; j += kBeamWarps) {
+                const int w = list[j] / S;
+                // the row's logits that may reach t0, rounded down
+                float lthr = -INFINITY;
+                if (t0 != -INFINITY) {
+                    const double l = static_cast<double>(rw.m[w]) + (t0 - rw.base[w]) / p.inv_t;
+                    lthr = static_cast<float>(l - fabs(l) * 1.2e-7);
+                }
+                gather_item<Tag>(p, b, w, list[j] - w * S, lthr, rw.base[w], rw.m[w], K, cand, a.cap, &ncand);
+            }
+        };
+        if (whole) {
+            gather(nlist);
+            __syncthreads();
+            whole = ncand <= a.cap;
+        }
+        if (!whole) {
+            // many equal maxima: exactly the K best items, one by one
+            int n = 0;
+            Cand last = {INFINITY, -1, -1};
+            __syncthreads();
+            if (tid == 0) ncand = 0;
+            __syncthreads();
+            if (tid < W && rw.kind[tid] == kRowDone) {
+                const int at = atomicAdd(&ncand, 1);
+                cand[at] = {static_cast<double>(rw.score[tid]), tid, a.end_token};
+            }
+            for (; n < min(K, kListMax); ++n) {
+                Cand top = {-INFINITY, INT_MAX, INT_MAX};
+                for (int i = tid; i < items; i += kBeamThreads) {
+                    const Cand c = {item_score(i), i / S, i - (i / S) * S};
+                    if (c.s > -INFINITY && better(last, c) && better(c, top)) top = c;
+                }
+#pragma unroll
+                for (int x = 16; x > 0; x >>= 1) {
+                    const Cand c = {__shfl_xor_sync(kFull, top.s, x), __shfl_xor_sync(kFull, top.w, x),
+                                    __shfl_xor_sync(kFull, top.v, x)};
+                    if (better(c, top)) top = c;
+                }
+                if (lane == 0) warp_best[warp] = top;
+                __syncthreads();
+                top = warp_best[0];
+                for (int i = 1; i < kBeamWarps; ++i)
+                    if (better(warp_best[i], top)) top = warp_best[i];
+                __syncthreads();
+                if (top.s == -INFINITY) break;
+                if (tid == 0) list[n] = top.w * S + top.v;
+                last = top;
+            }
+            __syncthreads();
+            gather(n);  // at most K candidates an item: they fit
+            __syncthreads();
+            if (tid == 0) nlist = n;
+        }
+        __syncthreads();
+
+        // rank every candidate; the first K are the selection
+        const int n = ncand;
+        found = min(n, K);
+        for (int i = tid; i < n; i += kBeamThreads) {
+            const Cand c = cand[i];
+            int rank = 0;
+            for (int j = 0; j < n && rank < K; ++j) rank += better(cand[j], c) ? 1 : 0;
+            if (rank < K) best[rank] = c;
+        }
+        __syncthreads();
+        // rows whose errors could change it
+        auto err = [&](int w) { return rw.kind[w] == kRowLive ? rw.err[w] : 0.0; };
+        auto close = [&](const Cand &x, double s, int w) {
+            const double e = err(x.w) + err(w);
+            return w != x.w && e > 0.0 && fabs(x.s - s) <= e;
+        };
+        auto want = [&](int w) {
+            if (rw.kind[w] == kRowLive && rw.err[w] > 0.0) {
+                rw.exact[w] = 1;
+                again = 1;
+            }
+        };
+        if (tid + 1 < found && close(best[tid], best[tid + 1].s, best[tid + 1].w)) {
+            want(best[tid].w);
+            want(best[tid + 1].w);
+        }
+        if (n > K || nlist > 0) {
+            if (found == K) {
+                const Cand kth = best[K - 1];
+                for (int i = tid; i < n; i += kBeamThreads) {
+                    const Cand c = cand[i];
+                    if (better(kth, c) && close(kth, c.s, c.w)) {
+                        want(kth.w);
+                        want(c.w);
+                    }
+                }
+                // items that are not in the list (their maxima)
+                for (int i = tid; i < items; i += kBeamThreads) {
+                    const double s = item_score(i);
+                    const int w = i / S;
+                    if (s == -INFINITY || !close(kth, s, w)) continue;
+                    bool in = false;
+                    for (int j = 0; j < nlist && !in; ++j) in = list[j] == i;
+                    if (!in) {
+                        want(kth.w);
+                        want(w);
+                    }
+                }
+            }
+        }
+        __syncthreads();
+        if (!again) break;
+        for (int j = tid; j < kExp2Tab; j += kBeamThreads) tab[j] = p.exp2tab[j];
+        __syncthreads();
+        for (int w = 0; w < W; ++w) {
+            if (rw.exact[w] != 1) continue;
+            const double sum = exact_sum<Tag>(p, b, w, rw.m[w], tab, scratch);
+            if (tid == 0) {
+                rw.base[w] = static_cast<double>(rw.score[w]) - log(sum);
+                rw.err[w] = 0.0;
+                rw.exact[w] = 2;
+            }
+        }
+        __syncthreads();
+    }
+    if (tid < K) {
+        const bool in = tid < found;
+        a.out_s[o + tid] = in ? static_cast<float>(best[tid].s) : -INFINITY;
+        a.out_p[o + tid] = in ? best[tid].w : -1;
+        a.out_t[o + tid] = in ? best[tid].v : -1;
+        if (a.out_f) a.out_f[o + tid] = in && best[tid].v == a.end_token ? 1 : 0;
+    }
+}
+
+constexpr size_t kBeamAlign = 256;
+int64_t ceil_div(int64_t x, int64_t y) { return (x + y - 1) / y; }
+
+// counters (one claim counter), then the pass-1 partials [B][W][S] (S of the
+// shorter fp32 items, so that both dtypes fit)
+size_t beam_bytes(int B, int W, int V)
+{
+    if (B < 0 || W < 1 || W > SPEC_MAX_BEAMS || V < 1) return 0;
+    const size_t s = static_cast<size_t>(ceil_div(V, Pass1Shape<F32>::kItem));
+    const size_t n = sizeof(float2) * static_cast<size_t>(B) * W * s;
+    return kBeamAlign + (n + kBeamAlign - 1) / kBeamAlign * kBeamAlign;
+}
+
+std::mutex g_beam_mu;
+int g_beam_blocks[64][2];
+int g_beam_sms[64];
+bool g_beam_attr[64][2];
+constexpr int kCandMin = 1024;
+size_t cand_count(int K) { return std::max(kCandMin, K * K) + SPEC_MAX_BEAMS; }
+
+template <class Tag>
+int launch_beam(Params &p, BeamArgs &a, int dtype_index, cudaStream_t st)
+{
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return SPEC_ECUDA;
+    int per_sm, sms;
+    {
+        std::lock_guard<std::mutex> lock(g_beam_mu);
+        if (g_beam_blocks[dev][dtype_index] < 1) {
+            int n = 0;
+            if (cudaFuncSetAttribute(k_pass1<Tag, kBeam, 2>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                     static_cast<int>(kRingBytes)) != cudaSuccess ||
+                cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, k_pass1<Tag, kBeam, 2>, kThreads, kRingBytes) !=
+                    cudaSuccess ||
+                n < 1)
+                return SPEC_ECUDA;
+            g_beam_blocks[dev][dtype_index] = n;
+        }
+        if (g_beam_sms[dev] < 1 &&
+            (cudaDeviceGetAttribute(&g_beam_sms[dev], cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
+             g_beam_sms[dev] < 1))
+            return SPEC_ECUDA;
+        if (!g_beam_attr[dev][dtype_index]) {
+            if (cudaFuncSetAttribute(k_beam_select<Tag>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                     static_cast<int>(sizeof(Cand) * cand_count(SPEC_MAX_BEAMS))) != cudaSuccess)
+                return SPEC_ECUDA;
+            g_beam_attr[dev][dtype_index] = true;
+        }
+        per_sm = g_beam_blocks[dev][dtype_index];
+        sms = g_beam_sms[dev];
+    }
+    const int64_t blocks =
+        std::max<int64_t>(1, std::min<int64_t>(static_cast<int64_t>(per_sm) * sms, ceil_div(p.nA, kWarps)));
+    const uint64_t warps = static_cast<uint64_t>(blocks) * kWarps;
+    p.nAs = static_cast<unsigned>((static_cast<uint64_t>(p.nA) * 88 / 100) / warps * warps);
+    if (cudaMemsetAsync(p.a_claim, 0xFF, sizeof(unsigned), st) != cudaSuccess) return SPEC_ECUDA;
+    k_pass1<Tag, kBeam, 2><<<static_cast<unsigned>(blocks), kThreads, kRingBytes, st>>>(p);
+    if (cudaGetLastError() != cudaSuccess) return SPEC_ECUDA;
+    a.cap = static_cast<int>(cand_count(a.keep));
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.gridDim = dim3(static_cast<unsigned>(p.B));
+    cfg.blockDim = dim3(kBeamThreads);
+    cfg.dynamicSmemBytes = sizeof(Cand) * static_cast<size_t>(a.cap);
+    cfg.stream = st;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaLaunchKernelEx(&cfg, k_beam_select<Tag>, p, a) != cudaSuccess) {
+        (void)cudaGetLastError();
+        return SPEC_ECUDA;
+    }
+    return SPEC_OK;
+}
+
+}  // namespace
+}  // namespace sv
+
+using namespace sv;
+
+extern "C" size_t spec_beam_workspace_size(int batch, int beams, int vocab)
+{
+    return beam_bytes(batch, beams, vocab);
+}
+
+extern "C" int spec_beam_select(const void *logits, spec_dtype_t dtype, int64_t row_stride,
+                                const float *scores, const int32_t *finished, int end_token,
+                                int batch, int beams, int vocab, float temperature, int keep,
+                                float *out_scores, int32_t *out_parents, int32_t *out_tokens,
+                                int32_t *out_finished, int32_t *status, void *workspace,
+                                size_t workspace_bytes, cudaStream_t stream)
+{
+    if (batch < 0 || beams < 1 || keep < 1) return SPEC_EINVAL;
+    if (beams > SPEC_MAX_BEAMS || keep > SPEC_MAX_BEAMS) return SPEC_EUNSUPPORTED;
+    if (!(temperature > 0.f) || !(temperature < INFINITY)) return SPEC_EINVAL;
+    if (!(static_cast<float>(1.4426950408889634074 / temperature) < INFINITY)) return SPEC_EINVAL;
+    if (dtype != SPEC_F32 && dtype != SPEC_BF16) return SPEC_EINVAL;
+    if (vocab < 1 || row_stride < vocab) return SPEC_EINVAL;
+    if (end_token < -1 || end_token >= vocab || (finished && end_token < 0)) return SPEC_EINVAL;
+    const int esz = dtype == SPEC_BF16 ? 2 : 4;
+    if ((row_stride * esz) % 16 != 0) return SPEC_EALIGN;
+    if (batch == 0) return SPEC_OK;
+    if (!logits || !scores || !out_scores || !out_parents || !out_tokens) return SPEC_EINVAL;
+    if ((reinterpret_cast<uintptr_t>(logits) & 15u) != 0) return SPEC_EALIGN;
+    const size_t need = beam_bytes(batch, beams, vocab);
+    if (!workspace || (reinterpret_cast<uintptr_t>(workspace) % kBeamAlign) != 0 || workspace_bytes < need)
+        return SPEC_EWORKSPACE;
+    const int S = static_cast<int>(
+        ceil_div(vocab, dtype == SPEC_BF16 ? Pass1Shape<Bf16>::kItem : Pass1Shape<F32>::kItem));
+    const int64_t nA = static_cast<int64_t>(batch) * beams * S;
+    if (nA >= (int64_t(1) << 31) || static_cast<int64_t>(batch) * keep > INT_MAX) return SPEC_EUNSUPPORTED;
+
+    Params p;
+    std::memset(&p, 0, sizeof p);
+    p.tl = logits;
+    p.stride = row_stride;
+    p.B = batch;
+    p.V = vocab;
+    p.R = beams;
+    p.S = S;
+    p.nA = static_cast<unsigned>(nA);
+    p.div_req = make_fastdiv(static_cast<uint32_t>(beams) * static_cast<uint32_t>(S));
+    p.div_s = make_fastdiv(static_cast<uint32_t>(S));
+    const double t = static_cast<double>(temperature);
+    p.inv_t = 1.0 / t;
+    p.c64 = 1.4426950408889634074 / t;
+    p.c = static_cast<float>(p.c64);
+    p.beam_scores = scores;
+    p.beam_done = finished;
+    p.status = status;
+    p.a_claim = static_cast<unsigned *>(workspace);
+    p.rowpart = reinterpret_cast<float2 *>(static_cast<char *>(workspace) + kBeamAlign);
+    for (int j = 0; j < kExp2Tab; ++j) p.exp2tab[j] = std::exp2(static_cast<double>(j) / kExp2Tab);
+    BeamArgs a{end_token, keep, 0, out_scores, out_parents, out_tokens, out_finished};
+    return dtype == SPEC_BF16 ? launch_beam<Bf16>(p, a, 1, stream) : launch_beam<F32>(p, a, 0, stream);
+}

@@ -221,6 +221,10 @@ __device__ __forceinline__ Item1 item1(const Params &p, unsigned item, bool chec
             base = p.dl;
             row = static_cast<int64_t>(b) * p.k + (r - p.k - 1);
         }
+    } else if (MODE == kBeam) {  // the rows of beams in use that have not ended
+        base = p.tl;
+        row = static_cast<int64_t>(b) * p.R + r;
+        it.active = __ldg(p.beam_scores + row) != -INFINITY && !(p.beam_done && __ldg(p.beam_done + row));
     } else if (r < p.N) {
         base = p.tl;
         row = static_cast<int64_t>(b) * p.N + r;
@@ -385,10 +389,27 @@ __device__ __forceinline__ void reduce_item1(const Params &p, unsigned item, int
         float acc[4];
         f2_unpack(acc2[0], acc[0], acc[1]);
         f2_unpack(acc2[1], acc[2], acc[3]);
-        const float lsum = (acc[0] + acc[1]) + (acc[2] + acc[3]);
+        float lsum = (acc[0] + acc[1]) + (acc[2] + acc[3]);
         const float M = warp_max_nan(m);
         float sr = 0.f;
-        if (m != -INFINITY) {
+        bool direct = false;
+        if (MODE == kBeam) {
+            // m c out of range (a lane of nothing but mask values near the
+            // type's lowest): the differences first
+            direct = fabsf(mc) == INFINITY && fabsf(m) < INFINITY;
+            if (direct) {
+                lsum = 0.f;
+#pragma unroll
+                for (int v = 0; v < kV; ++v) {
+                    float x[kVec];
+                    unpack<Tag>(raw[v], x);
+#pragma unroll
+                    for (int e = 0; e < kVec; ++e) lsum += ex2_approx((x[e] - m) * c);
+                }
+                sr = lsum * ex2_approx((m - M) * c);
+            }
+        }
+        if (m != -INFINITY && !direct) {
             const float d = -fmaf(m, c, nmc);  // fl(m c) - m c, exactly
             sr = lsum * ex2_approx((m - M) * c) * fmaf(d, 0.693147180559945309f, 1.0f);
         }

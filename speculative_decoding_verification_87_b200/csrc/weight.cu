@@ -4,11 +4,27 @@
 // Mathematics.  With s_rt = scale q_r . k_t over the rows r = (query i,
 // head g of the group), slot t gains sum_r exp(s_rt - L_r) where L_r is the
 // row's log-sum-exp over the slots it sees (t <= begin + i).  L_r needs every
-// slot of the row before the first weight can be formed, hence three steps:
-// partial (max, sum) per row and chunk of slots, their merge into L_r, the
-// weights.  A slot's weights are summed by one thread in row order, so the
-// result does not depend on the schedule.  Everything is in units of log2
-// (scale log2 e folded into the products), sums and statistics in fp32.
+// slot of the row before the first weight can be formed.  Everything is in
+// units of log2 (scale log2 e multiplies the products), sums and statistics
+// in fp32.
+//
+// One kernel: a cluster of blocks per (request, head), each with a slice of
+// the slots.  The products go to the block's shared memory, become
+// e = 2^(s - m) with the block's own row maxima m there, the blocks exchange
+// (m, sum e) per row through distributed shared memory, and slot t gains
+// sum_r e_rt 2^(m_r - L_r): the keys are read once and there is one
+// exponential per product.  A slice whose products do not fit is swept in
+// parts twice, once for the statistics and once for the weights.
+//
+// Products run on mma.sync m16n8k16 with the slots as rows of A, read
+// straight from global memory into fragments: the sum over d may run in any
+// order, so a lane's 16 contiguous bytes (8 elements) of a key serve as its
+// two k-steps' elements, with the queries laid out the same way.  fp32
+// inputs are split into three bf16 parts (24 bits in all) and the six
+// products above 2^-24 are added up.
+//
+// A slot's weights are summed by one thread in row order and the parts are
+// merged in a fixed order, so results do not depend on the schedule.
 #include <algorithm>
 #include <climits>
 #include <cmath>
@@ -16,6 +32,8 @@
 #include <cstring>
 #include <mutex>
 
+#include <cooperative_groups.h>
+#include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
 #include "../../include/specverify.h"
@@ -24,26 +42,31 @@
 namespace sv {
 namespace {
 
-constexpr int kTile = 128;      // slots per tile, a thread each
-constexpr int kRows = 8;        // rows per register tile
-constexpr int kChunksMax = 64;  // chunks of slots per row
+namespace cg = cooperative_groups;
+
+constexpr int kScoreThreads = 256;
+constexpr int kScoreWarps = kScoreThreads / 32;
+constexpr int kGroup = 4;           // n-tiles (8 rows each) per register group
+constexpr int kClusterMax = 16;
+constexpr int kPartSlots = 128;     // a swept part is a multiple of this: 16 slots a warp
 
 struct ScoreArgs {
     const void *q, *k;
     int64_t q_req, q_tok, q_head, k_req, k_head, k_slot;  // elements
     const int32_t *begin, *end;
     int B, Q, H, G, D, C;  // H key heads, C capacity
-    int R;                 // Q * G
-    int chunk, chunks;     // slots per chunk, chunks per row
+    int blocks;            // of a cluster
+    int tile_rows;         // rows of a row tile (a multiple of 8)
+    int held_rows;         // of them, rows whose products are stored
+    int part;              // slots whose products fit shared memory
+    int pitch;             // words between rows of products
     float scale2;          // scale * log2(e)
     const float *in;
     float *out;
     int32_t *status;
-    float2 *part;          // [B][H][R][chunks]
-    float *lse;            // [B][H][R], log2 units
 };
 
-// Filled slots and queries of request b; false: left as it was.
+// Filled slots and queries of request b; !ok: left as it was.
 struct Span {
     int begin, end;
     bool ok;
@@ -57,226 +80,402 @@ __device__ __forceinline__ Span span_of(const ScoreArgs &a, int b)
     return s;
 }
 
-// Row r = i * G + g of head h: its first element.
-template <class Tag>
-__device__ __forceinline__ const typename Tag::elem *row_at(const ScoreArgs &a, int b, int h, int r)
-{
-    const int i = r / a.G, g = r - i * a.G;
-    return static_cast<const typename Tag::elem *>(a.q) + b * a.q_req + i * a.q_tok +
-           (static_cast<int64_t>(h) * a.G + g) * a.q_head;
-}
-
-// Rows [r0, r0 + kRows) below `rows` into shared memory as fp32, times
-// scale2; the rest as zeros.
-template <class Tag>
-__device__ __forceinline__ void stage_rows(const ScoreArgs &a, int b, int h, int r0, int rows, float *sq)
-{
-    constexpr int kVec = Tag::kVec;
-    const int nv = a.D / kVec;
-    for (int i = threadIdx.x; i < kRows * nv; i += kTile) {
-        const int r = i / nv, v = i - r * nv;
-        float x[kVec];
-        if (r0 + r < rows) unpack<Tag>(ldg_vec(row_at<Tag>(a, b, h, r0 + r) + v * kVec), x);
-#pragma unroll
-        for (int e = 0; e < kVec; ++e) sq[r * a.D + v * kVec + e] = r0 + r < rows ? x[e] * a.scale2 : 0.f;
-    }
-}
-
-// Slots [t0, t0 + kTile) below `end` into shared memory as fp32 (pitch
-// D + 4 words), the rest as zeros.
-template <class Tag>
-__device__ __forceinline__ void stage_slots(const ScoreArgs &a, int b, int h, int t0, int end, float *sk)
-{
-    constexpr int kVec = Tag::kVec;
-    const int nv = a.D / kVec, pitch = a.D + 4;
-    const auto *base = static_cast<const typename Tag::elem *>(a.k) + b * a.k_req + h * a.k_head;
-    for (int i = threadIdx.x; i < kTile * nv; i += kTile) {
-        const int t = i / nv, v = i - t * nv;
-        float x[kVec];
-        if (t0 + t < end) {
-            unpack<Tag>(ldg_vec(base + (t0 + t) * a.k_slot + v * kVec), x);
-        } else {
-#pragma unroll
-            for (int e = 0; e < kVec; ++e) x[e] = 0.f;
-        }
-#pragma unroll
-        for (int e = 0; e < kVec; ++e) sk[t * pitch + v * kVec + e] = x[e];
-    }
-}
-
-// This thread's slot against the staged rows.
-__device__ __forceinline__ void products(const float *sq, const float *sk, int D, float (&s)[kRows])
-{
-    const float *mine = sk + threadIdx.x * (D + 4);
-#pragma unroll
-    for (int r = 0; r < kRows; ++r) s[r] = 0.f;
-    for (int d = 0; d < D; d += 4) {
-        const float4 x = *reinterpret_cast<const float4 *>(mine + d);
-#pragma unroll
-        for (int r = 0; r < kRows; ++r) {
-            const float4 y = *reinterpret_cast<const float4 *>(sq + r * D + d);
-            s[r] = fmaf(x.x, y.x, fmaf(x.y, y.y, fmaf(x.z, y.z, fmaf(x.w, y.w, s[r]))));
-        }
-    }
-}
-
 // Merge (m, l) pairs, l relative to 2^m; an empty pair is (-inf, 0).
 __device__ __forceinline__ void merge(float &m, float &l, float om, float ol)
 {
     const float n = max_nan(m, om);
     if (n == -INFINITY) return;
-    l = l * exp2f(m - n) + ol * exp2f(om - n);
+    l = l * ex2_approx(m - n) + ol * ex2_approx(om - n);
     m = n;
 }
 
-// Partial statistics: grid (row tile * chunks + chunk, head, request).
-template <class Tag>
-__global__ void __launch_bounds__(kTile) k_score_stats(const __grid_constant__ ScoreArgs a)
+__device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                         uint32_t b0, uint32_t b1)
 {
-    extern __shared__ __align__(16) float smem[];
-    float *sq = smem, *sk = smem + kRows * a.D;
-    __shared__ float2 warp_part[kTile / 32][kRows];
-    const int b = blockIdx.z, h = blockIdx.y;
-    const int r0 = static_cast<int>(blockIdx.x / a.chunks) * kRows, chunk = blockIdx.x % a.chunks;
-    const Span sp = span_of(a, b);
-    const int rows = (sp.end - sp.begin) * a.G;
-    if (!sp.ok || r0 >= rows) return;
-    const int t_begin = chunk * a.chunk, t_end = min(sp.end, t_begin + a.chunk);
-    float m[kRows], l[kRows];
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+                 "{%0,%1,%2,%3};\n"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// Eight elements of a vector as bf16 pairs: themselves, or the three parts
+// of fp32 values (x = p0 + p1 + p2 to 24 bits, each difference exact).
+__device__ __forceinline__ uint32_t pack2(float lo, float hi)
+{
+    const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+template <class Tag>
+struct Parts;
+template <>
+struct Parts<Bf16> {
+    static constexpr int kRaw = 1;   // uint4 of raw data per 8 elements
+    static constexpr int kParts = 1;
+    static __device__ __forceinline__ void split(const uint4 (&raw)[1], uint4 (&p)[1]) { p[0] = raw[0]; }
+};
+template <>
+struct Parts<F32> {
+    static constexpr int kRaw = 2;
+    static constexpr int kParts = 3;
+    static __device__ __forceinline__ void split(const uint4 (&raw)[2], uint4 (&p)[3])
+    {
+        float x[8] = {__uint_as_float(raw[0].x), __uint_as_float(raw[0].y), __uint_as_float(raw[0].z),
+                      __uint_as_float(raw[0].w), __uint_as_float(raw[1].x), __uint_as_float(raw[1].y),
+                      __uint_as_float(raw[1].z), __uint_as_float(raw[1].w)};
 #pragma unroll
-    for (int r = 0; r < kRows; ++r) {
-        m[r] = -INFINITY;
-        l[r] = 0.f;
+        for (int i = 0; i < 3; ++i) {
+            uint32_t w[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                w[e] = pack2(x[2 * e], x[2 * e + 1]);
+                x[2 * e] -= bf16_lo(w[e]);
+                x[2 * e + 1] -= bf16_hi(w[e]);
+            }
+            p[i] = make_uint4(w[0], w[1], w[2], w[3]);
+        }
     }
-    stage_rows<Tag>(a, b, h, r0, rows, sq);
-    for (int t0 = t_begin; t0 < t_end; t0 += kTile) {
-        __syncthreads();
-        stage_slots<Tag>(a, b, h, t0, t_end, sk);
-        __syncthreads();
-        float s[kRows];
-        products(sq, sk, a.D, s);
-        const int t = t0 + threadIdx.x;
+};
+
+// Elements d .. d + 7 of a row of D elements (zeros past D).
+template <class Tag>
+__device__ __forceinline__ void load8(const typename Tag::elem *row, int d, int D, uint4 (&raw)[Parts<Tag>::kRaw])
+{
 #pragma unroll
-        for (int r = 0; r < kRows; ++r)
-            if (t < t_end && t <= sp.begin + (r0 + r) / a.G) merge(m[r], l[r], s[r], 1.f);
-    }
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-#pragma unroll
-    for (int r = 0; r < kRows; ++r) {
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1)
-            merge(m[r], l[r], __shfl_xor_sync(kFull, m[r], o), __shfl_xor_sync(kFull, l[r], o));
-        if (lane == 0) warp_part[warp][r] = make_float2(m[r], l[r]);
-    }
-    __syncthreads();
-    if (threadIdx.x < kRows && r0 + threadIdx.x < rows) {
-        float2 x = warp_part[0][threadIdx.x];
-        for (int w = 1; w < kTile / 32; ++w) merge(x.x, x.y, warp_part[w][threadIdx.x].x, warp_part[w][threadIdx.x].y);
-        a.part[((static_cast<int64_t>(b) * a.H + h) * a.R + r0 + threadIdx.x) * a.chunks + chunk] = x;
+    for (int i = 0; i < Parts<Tag>::kRaw; ++i) {
+        raw[i] = make_uint4(0u, 0u, 0u, 0u);
+        if (d + i * Tag::kVec < D) raw[i] = ldg_vec(row + d + i * Tag::kVec);
     }
 }
 
-// L_r of every row: a warp each.
-__global__ void __launch_bounds__(256) k_score_merge(const __grid_constant__ ScoreArgs a)
+// A warp's 16 slots: lane (g = lane / 4, t = lane % 4) holds elements
+// 32 j + 8 t .. + 7 of slots g and g + 8.  Up to 128 bf16 elements are held
+// in registers, loaded ahead of use (kHeld); longer or fp32 rows, which would
+// not fit beside the accumulators, are read where they are used, from L1
+// after the first group of rows.
+template <class Tag, int NB>
+struct Slots {
+    static constexpr bool kHeld = Parts<Tag>::kParts == 1 && NB <= 4;
+    uint4 raw[kHeld ? NB : 1][2][Parts<Tag>::kRaw];
+    const typename Tag::elem *row[2];
+    int width[2];  // D, or 0 past the last slot
+    __device__ __forceinline__ void load(const ScoreArgs &a, const typename Tag::elem *keys, int t0, int end)
+    {
+        const int lane = threadIdx.x & 31;
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            const int slot = t0 + (lane >> 2) + 8 * half;
+            row[half] = keys + slot * a.k_slot;
+            width[half] = slot < end ? a.D : 0;
+            if (kHeld) {
+#pragma unroll
+                for (int j = 0; j < NB; ++j)
+                    load8<Tag>(row[half], 32 * j + 8 * (lane & 3), width[half], raw[kHeld ? j : 0][half]);
+            }
+        }
+    }
+    __device__ __forceinline__ void part(int j, int half, uint4 (&p)[Parts<Tag>::kParts]) const
+    {
+        if (kHeld) {
+            Parts<Tag>::split(raw[kHeld ? j : 0][half], p);
+        } else {
+            uint4 x[Parts<Tag>::kRaw];
+            load8<Tag>(row[half], 32 * j + 8 * (threadIdx.x & 3), width[half], x);
+            Parts<Tag>::split(x, p);
+        }
+    }
+};
+
+// Rows [r0, r0 + 8 * tiles) of head h below `rows`, as B fragments: 512
+// bytes per (n-tile, 32 elements, part), a lane's 16 bytes in place.
+template <class Tag, int NB>
+__device__ __forceinline__ void stage_rows(const ScoreArgs &a, int b, int h, int r0, int rows, int tiles, uint4 *sq)
 {
+    constexpr int kP = Parts<Tag>::kParts;
+    const int nb = (a.D + 31) / 32;
+    for (int i = threadIdx.x; i < tiles * nb * 32; i += kScoreThreads) {
+        const int lane = i & 31, j = (i >> 5) % nb, tile = (i >> 5) / nb;
+        const int r = r0 + tile * 8 + (lane >> 2);
+        uint4 raw[Parts<Tag>::kRaw], p[kP];
+        const int q = r / a.G, g = r - q * a.G;
+        const auto *row = static_cast<const typename Tag::elem *>(a.q) + b * a.q_req + q * a.q_tok +
+                          (static_cast<int64_t>(h) * a.G + g) * a.q_head;
+        load8<Tag>(row, r < rows ? 32 * j + 8 * (lane & 3) : a.D, a.D, raw);
+        Parts<Tag>::split(raw, p);
+#pragma unroll
+        for (int x = 0; x < kP; ++x) sq[((tile * nb + j) * kP + x) * 32 + lane] = p[x];
+    }
+}
+
+// The products of a warp's 16 slots with n-tiles [tile0, tile0 + kGroup):
+// fp32 accumulators, c[n][0..1] slot g rows 2t, 2t+1; c[n][2..3] slot g + 8.
+template <class Tag, int NB>
+__device__ __forceinline__ void products(const Slots<Tag, NB> &k, const uint4 *sq, int nb, int tile0, int tiles,
+                                         float (&c)[kGroup][4])
+{
+    constexpr int kP = Parts<Tag>::kParts;
     const int lane = threadIdx.x & 31;
-    const int64_t row = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) >> 5;
-    if (row >= static_cast<int64_t>(a.B) * a.H * a.R) return;
-    const int b = static_cast<int>(row / (static_cast<int64_t>(a.H) * a.R)), r = static_cast<int>(row % a.R);
-    const Span sp = span_of(a, b);
-    if (!sp.ok || r >= (sp.end - sp.begin) * a.G) return;
-    const int n = (sp.end + a.chunk - 1) / a.chunk;
-    float m = -INFINITY, l = 0.f;
-    for (int c = lane; c < n; c += 32) {
-        const float2 x = __ldcg(a.part + row * a.chunks + c);
-        merge(m, l, x.x, x.y);
-    }
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) merge(m, l, __shfl_xor_sync(kFull, m, o), __shfl_xor_sync(kFull, l, o));
-    if (lane == 0) a.lse[row] = m + log2f(l);
+    for (int n = 0; n < kGroup; ++n) c[n][0] = c[n][1] = c[n][2] = c[n][3] = 0.f;
+#pragma unroll
+    for (int j = 0; j < NB; ++j) {
+        if (j < nb) {
+            uint4 lo[kP], hi[kP];
+            k.part(j, 0, lo);
+            k.part(j, 1, hi);
+#pragma unroll
+            for (int n = 0; n < kGroup; ++n) {
+                if (tile0 + n < tiles) {
+                    uint4 y[kP];
+#pragma unroll
+                    for (int x = 0; x < kP; ++x) y[x] = sq[(((tile0 + n) * nb + j) * kP + x) * 32 + lane];
+                    // the smaller products first
+#pragma unroll
+                    for (int s = kP - 1; s >= 0; --s)
+#pragma unroll
+                        for (int x = s; x >= 0; --x) {
+                            const uint4 u = lo[x], v = hi[x], w = y[s - x];
+                            mma_bf16(c[n], u.x, v.x, u.y, v.y, w.x, w.y);
+                            mma_bf16(c[n], u.z, v.z, u.w, v.w, w.z, w.w);
+                        }
+                }
+            }
+        }
+    }
 }
 
-// The weights: grid (tile of slots, head, request).
-template <class Tag>
-__global__ void __launch_bounds__(kTile) k_score_apply(const __grid_constant__ ScoreArgs a)
+template <class Tag, int NB>
+__global__ void __launch_bounds__(kScoreThreads, 2) k_score(const __grid_constant__ ScoreArgs a)
 {
-    extern __shared__ __align__(16) float smem[];
-    float *sq = smem, *sk = smem + kRows * a.D;
-    __shared__ float lse[kRows];
-    const int b = blockIdx.z, h = blockIdx.y, t0 = static_cast<int>(blockIdx.x) * kTile;
+    extern __shared__ __align__(16) unsigned char smem[];
+    cg::cluster_group cluster = cg::this_cluster();
+    const int rank = static_cast<int>(cluster.block_rank()), blocks = a.blocks;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int64_t head = blockIdx.x / blocks;
+    const int b = static_cast<int>(head / a.H), h = static_cast<int>(head % a.H);
     const Span sp = span_of(a, b);
-    if (!sp.ok) {
-        if (threadIdx.x == 0 && blockIdx.x == 0 && h == 0 && a.status) atomicOr(a.status, SPEC_STATUS_CAPACITY);
+    if (!sp.ok) {  // the whole cluster leaves
+        if (tid == 0 && rank == 0 && h == 0 && a.status) atomicOr(a.status, SPEC_STATUS_CAPACITY);
         return;
     }
-    if (t0 >= sp.end) return;
+    const int nb = (a.D + 31) / 32;
+    // shared memory: query fragments, products, row statistics and factors
+    uint4 *sq = reinterpret_cast<uint4 *>(smem);
+    float *ss = reinterpret_cast<float *>(sq + a.tile_rows / 8 * nb * Parts<Tag>::kParts * 32);
+    float2 *stat = reinterpret_cast<float2 *>(ss + a.held_rows * a.pitch);  // [units]
+    float *fac = reinterpret_cast<float *>(stat + max(a.tile_rows, kScoreWarps));               // [units]
+
     const int rows = (sp.end - sp.begin) * a.G;
-    const int t = t0 + threadIdx.x;
-    const int64_t at = (static_cast<int64_t>(b) * a.H + h) * a.C + t;
-    float sum = 0.f;
-    stage_slots<Tag>(a, b, h, t0, sp.end, sk);
-    for (int r0 = 0; r0 < rows; r0 += kRows) {
-        __syncthreads();
-        stage_rows<Tag>(a, b, h, r0, rows, sq);
-        if (threadIdx.x < kRows)
-            lse[threadIdx.x] = r0 + threadIdx.x < rows
-                                   ? __ldcg(a.lse + (static_cast<int64_t>(b) * a.H + h) * a.R + r0 + threadIdx.x)
-                                   : 0.f;
-        __syncthreads();
-        float s[kRows];
-        products(sq, sk, a.D, s);
-#pragma unroll
-        for (int r = 0; r < kRows; ++r)
-            if (r0 + r < rows && t <= sp.begin + (r0 + r) / a.G) sum += exp2f(s[r] - lse[r]);
+    const auto *keys = static_cast<const typename Tag::elem *>(a.k) + b * a.k_req + h * a.k_head;
+    const float *in = a.in + head * a.C;
+    float *out = a.out + head * a.C;
+    // the block's slots, whole m-tiles
+    const int slice = ((sp.end + blocks - 1) / blocks + 15) / 16 * 16;
+    const int s0 = min(sp.end, rank * slice), s1 = min(sp.end, s0 + slice);
+    const bool once = s1 - s0 <= a.part;
+
+    if (rows == 0) {
+        for (int t = s0 + tid; t < s1; t += kScoreThreads) out[t] = in[t];
+        return;
     }
-    if (t < sp.end) a.out[at] = (t < sp.begin ? a.in[at] : 0.f) + sum;
+    for (int r0 = 0; r0 < rows; r0 += a.tile_rows) {
+        const int nr = min(rows - r0, a.tile_rows), tiles = (nr + 7) / 8;
+        // a row's slots are shared by `split` warps where rows are few
+        const int split = nr <= 1 ? 8 : nr <= 2 ? 4 : nr <= 4 ? 2 : 1;
+        __syncthreads();
+        stage_rows<Tag, NB>(a, b, h, r0, rows, tiles, sq);
+        for (int i = tid; i < nr * split; i += kScoreThreads) stat[i] = make_float2(-INFINITY, 0.f);
+        __syncthreads();
+
+        // products of slots [p0, p1) into ss[row][slot - p0], -inf where unseen
+        auto fill = [&](int p0, int p1) {
+            Slots<Tag, NB> cur, next;
+            int t0 = p0 + warp * 16;
+            if (t0 < p1) cur.load(a, keys, t0, p1);
+            for (; t0 < p1; t0 += kScoreWarps * 16) {
+                if (t0 + kScoreWarps * 16 < p1) next.load(a, keys, t0 + kScoreWarps * 16, p1);
+                const int g = lane >> 2, t2 = 2 * (lane & 3);
+                for (int tile0 = 0; tile0 < tiles; tile0 += kGroup) {
+                    float c[kGroup][4];
+                    products<Tag, NB>(cur, sq, nb, tile0, tiles, c);
+#pragma unroll
+                    for (int n = 0; n < kGroup; ++n) {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const int r = (tile0 + n) * 8 + t2 + (e & 1), t = t0 + g + 8 * (e >> 1);
+                            if (r < nr) {
+                                const bool seen = t < p1 && (t <= sp.begin || t <= sp.begin + (r0 + r) / a.G);
+                                ss[r * a.pitch + t - p0] = seen ? c[n][e] * a.scale2 : -INFINITY;
+                            }
+                        }
+                    }
+                }
+                cur = next;
+            }
+        };
+        // row statistics of the part, merged into stat; with `keep` the
+        // products become 2^(s - m)
+        auto statistics = [&](int n, bool keep) {
+            const int span = ((n + split - 1) / split + 31) / 32 * 32;
+            for (int u = warp; u < nr * split; u += kScoreWarps) {
+                float *row = ss + (u / split) * a.pitch;
+                const int i0 = min(n, (u % split) * span), i1 = min(n, i0 + span);
+                float m = -INFINITY;
+                for (int i = i0 + lane; i < i1; i += 32) m = max_nan(m, row[i]);
+                m = warp_max_nan(m);
+                float l = 0.f;
+                if (m != -INFINITY || keep)
+                    for (int i = i0 + lane; i < i1; i += 32) {
+                        const float e = m == -INFINITY ? 0.f : ex2_approx(row[i] - m);
+                        l += e;
+                        if (keep) row[i] = e;
+                    }
+                l = warp_sum(l);
+                if (lane == 0) {
+                    float2 x = stat[u];
+                    merge(x.x, x.y, m, l);
+                    stat[u] = x;
+                }
+            }
+        };
+        // slots [p0, p1): the weights of this row tile, from 2^(s - m) and
+        // factors, or from the products and L
+        auto apply = [&](int p0, int p1, bool kept) {
+            const int n = p1 - p0;
+            const int span = ((n + split - 1) / split + 31) / 32 * 32;
+            for (int i = tid; i < n; i += kScoreThreads) {
+                const int t = p0 + i;
+                const float *col = ss + i;
+                float sum = 0.f;
+                if (t <= sp.begin) {  // seen by every row
+                    if (kept) {
+                        const float *f = fac + i / span;
+                        for (int r = 0; r < nr; ++r) sum = fmaf(col[r * a.pitch], f[r * split], sum);
+                    } else {
+                        for (int r = 0; r < nr; ++r) sum += ex2_approx(col[r * a.pitch] - fac[r]);
+                    }
+                } else {
+                    const int first = max(0, (t - sp.begin) * a.G - r0);
+                    for (int r = first; r < nr; ++r)
+                        sum += kept ? col[r * a.pitch] * fac[r * split + i / span] : ex2_approx(col[r * a.pitch] - fac[r]);
+                }
+                const float old = r0 > 0 ? out[t] : t < sp.begin ? in[t] : 0.f;
+                out[t] = old + sum;
+            }
+        };
+
+        for (int p0 = s0; p0 < s1; p0 += a.part) {
+            const int p1 = min(s1, p0 + a.part);
+            fill(p0, p1);
+            __syncthreads();
+            statistics(p1 - p0, once);
+            __syncthreads();
+        }
+        // L of every row, from all blocks and splits in a fixed order
+        cluster.sync();
+        for (int r = tid; r < nr; r += kScoreThreads) {
+            float m = -INFINITY, l = 0.f;
+            for (int k = 0; k < blocks; ++k) {
+                const float2 *other = cluster.map_shared_rank(stat, k);
+                for (int x = 0; x < split; ++x) {
+                    const float2 y = other[r * split + x];
+                    merge(m, l, y.x, y.y);
+                }
+            }
+            const float L = m + log2f(l);
+            for (int x = 0; x < split; ++x)
+                fac[once ? r * split + x : r] = once ? ex2_approx(stat[r * split + x].x - L) : L;
+        }
+        cluster.sync();  // stat is read everywhere; fac is complete here
+        for (int p0 = s0; p0 < s1; p0 += a.part) {
+            const int p1 = min(s1, p0 + a.part);
+            if (!once) {
+                fill(p0, p1);
+                __syncthreads();
+            }
+            apply(p0, p1, once);
+            __syncthreads();
+        }
+    }
 }
 
 constexpr size_t kScoreAlign = 256;
 int64_t ceil_div(int64_t x, int64_t y) { return (x + y - 1) / y; }
-size_t align_up(size_t x) { return (x + kScoreAlign - 1) / kScoreAlign * kScoreAlign; }
 
-// Slots per chunk: at most kChunksMax chunks, whole tiles.
-int chunk_slots(int C) { return static_cast<int>(ceil_div(ceil_div(C, kChunksMax), kTile) * kTile); }
-
-struct ScoreLayout {
-    size_t part, lse, total;
+// How a call is laid out: blocks of a cluster, rows of a row tile, slots whose
+// products fit.  Two blocks share an SM (110 KB each).
+constexpr size_t kScoreSmem = 110 * 1024;
+struct ScorePlan {
+    int blocks, tile_rows, held_rows, part, pitch;
+    size_t smem;
 };
-bool score_layout(int B, int Q, int Hq, int H, int C, ScoreLayout &L)
+ScorePlan score_plan(int B, int H, int R, int D, int C, bool f32)
 {
-    if (B < 0 || Q < 1 || H < 1 || Hq < H || Hq % H != 0 || C < 1) return false;
-    const size_t rows = static_cast<size_t>(B) * Hq * Q;
-    L.part = 0;
-    L.lse = align_up(sizeof(float2) * rows * ceil_div(C, chunk_slots(C)));
-    L.total = std::max(kScoreAlign, L.lse + align_up(sizeof(float) * rows));
-    return true;
+    ScorePlan p;
+    // rows of a tile: their fragments, statistics and at least kPartSlots products
+    const int64_t row_bytes = ceil_div(D, 32) * 64 * (f32 ? 3 : 1) + 4 * (kPartSlots + 36) + 12;
+    const int64_t most = std::min<int64_t>(128, (kScoreSmem - 96) / row_bytes / 8 * 8);
+    const int64_t tiles = ceil_div(R, most);
+    p.tile_rows = static_cast<int>(ceil_div(ceil_div(R, tiles), 8) * 8);
+    p.held_rows = std::min(R, p.tile_rows);
+    const size_t frag = static_cast<size_t>(p.tile_rows) * ceil_div(D, 32) * 64 * (f32 ? 3 : 1);
+    const size_t stat = static_cast<size_t>(std::max(p.tile_rows, kScoreWarps)) * 12;
+    const int64_t words = static_cast<int64_t>((kScoreSmem - frag - stat) / 4 / static_cast<size_t>(p.held_rows));
+    // enough blocks for two on every SM, and so many that the slices fit
+    p.blocks = 1;
+    while (p.blocks < kClusterMax && p.blocks * kPartSlots < C &&
+           (static_cast<int64_t>(B) * H * p.blocks < 2 * 148 || ceil_div(C, p.blocks) + 36 > words))
+        p.blocks *= 2;
+    const int64_t slice = ceil_div(ceil_div(C, p.blocks), 16) * 16;
+    p.part = static_cast<int>(slice + 36 <= words ? slice : (words - 36) / kPartSlots * kPartSlots);
+    p.pitch = static_cast<int>(ceil_div(p.part, 32) * 32 + 4);
+    p.smem = frag + stat + sizeof(float) * static_cast<size_t>(p.pitch) * p.held_rows;
+    return p;
 }
 
 std::mutex g_score_mu;
-bool g_score_attr[64][2];
+bool g_score_attr[64][2][3];
 
-template <class Tag>
-int launch_score(const ScoreArgs &a, int dtype_index, cudaStream_t st)
+template <class Tag, int NB>
+int launch_score(const ScoreArgs &a, size_t smem, int dtype_index, int nb_index, cudaStream_t st)
 {
-    const size_t smem = sizeof(float) * (static_cast<size_t>(kRows) * a.D + static_cast<size_t>(kTile) * (a.D + 4));
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return SPEC_ECUDA;
     {
         std::lock_guard<std::mutex> lock(g_score_mu);
-        if (!g_score_attr[dev][dtype_index]) {
-            const int most = static_cast<int>(sizeof(float) * (kRows * SPEC_MAX_HEAD_DIM + kTile * (SPEC_MAX_HEAD_DIM + 4)));
-            if (cudaFuncSetAttribute(k_score_stats<Tag>, cudaFuncAttributeMaxDynamicSharedMemorySize, most) != cudaSuccess ||
-                cudaFuncSetAttribute(k_score_apply<Tag>, cudaFuncAttributeMaxDynamicSharedMemorySize, most) != cudaSuccess)
+        if (!g_score_attr[dev][dtype_index][nb_index]) {
+            if (cudaFuncSetAttribute(k_score<Tag, NB>, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024) !=
+                    cudaSuccess ||
+                cudaFuncSetAttribute(k_score<Tag, NB>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) !=
+                    cudaSuccess)
                 return SPEC_ECUDA;
-            g_score_attr[dev][dtype_index] = true;
+            g_score_attr[dev][dtype_index][nb_index] = true;
         }
     }
-    const unsigned H = static_cast<unsigned>(a.H), B = static_cast<unsigned>(a.B);
-    const unsigned tiles = static_cast<unsigned>(ceil_div(a.R, kRows) * a.chunks);
-    k_score_stats<Tag><<<dim3(tiles, H, B), kTile, smem, st>>>(a);
-    k_score_merge<<<static_cast<unsigned>(ceil_div(static_cast<int64_t>(a.B) * a.H * a.R, 8)), 256, 0, st>>>(a);
-    k_score_apply<Tag><<<dim3(static_cast<unsigned>(ceil_div(a.C, kTile)), H, B), kTile, smem, st>>>(a);
-    return cudaGetLastError() == cudaSuccess ? SPEC_OK : SPEC_ECUDA;
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = static_cast<unsigned>(a.blocks);
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.gridDim = dim3(static_cast<unsigned>(static_cast<int64_t>(a.B) * a.H * a.blocks));
+    cfg.blockDim = dim3(kScoreThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaLaunchKernelEx(&cfg, k_score<Tag, NB>, a) != cudaSuccess) {
+        (void)cudaGetLastError();
+        return SPEC_ECUDA;
+    }
+    return SPEC_OK;
+}
+
+template <class Tag>
+int launch_score(const ScoreArgs &a, size_t smem, int dtype_index, cudaStream_t st)
+{
+    if (a.D <= 64) return launch_score<Tag, 2>(a, smem, dtype_index, 0, st);
+    if (a.D <= 128) return launch_score<Tag, 4>(a, smem, dtype_index, 1, st);
+    return launch_score<Tag, 8>(a, smem, dtype_index, 2, st);
 }
 
 }  // namespace
@@ -286,8 +485,9 @@ using namespace sv;
 
 extern "C" size_t spec_score_workspace_size(int batch, int queries, int q_heads, int kv_heads, int capacity)
 {
-    ScoreLayout L;
-    return score_layout(batch, queries, q_heads, kv_heads, capacity, L) ? L.total : 0;
+    if (batch < 0 || queries < 1 || kv_heads < 1 || q_heads < kv_heads || q_heads % kv_heads != 0 || capacity < 1)
+        return 0;
+    return kScoreAlign;
 }
 
 extern "C" int spec_cache_score(const void *q, const void *k, spec_dtype_t dtype, int64_t q_request_stride,
@@ -319,10 +519,12 @@ extern "C" int spec_cache_score(const void *q, const void *k, spec_dtype_t dtype
     if (batch == 0) return SPEC_OK;
     if (!q || !k || !begin || !end || !scores || !out_scores) return SPEC_EINVAL;
     if (((reinterpret_cast<uintptr_t>(q) | reinterpret_cast<uintptr_t>(k)) & 15u) != 0) return SPEC_EALIGN;
-    ScoreLayout L;
-    if (!score_layout(batch, queries, q_heads, kv_heads, capacity, L)) return SPEC_EINVAL;
-    if (!workspace || (reinterpret_cast<uintptr_t>(workspace) % kScoreAlign) != 0 || workspace_bytes < L.total)
+    if (!workspace || (reinterpret_cast<uintptr_t>(workspace) % kScoreAlign) != 0 || workspace_bytes < kScoreAlign)
         return SPEC_EWORKSPACE;
+    const bool f32 = dtype == SPEC_F32;
+    const ScorePlan plan =
+        score_plan(batch, kv_heads, queries * (q_heads / kv_heads), head_dim, capacity, f32);
+    if (static_cast<int64_t>(batch) * kv_heads * plan.blocks > INT_MAX) return SPEC_EUNSUPPORTED;
     ScoreArgs a;
     std::memset(&a, 0, sizeof a);
     a.q = q;
@@ -341,14 +543,14 @@ extern "C" int spec_cache_score(const void *q, const void *k, spec_dtype_t dtype
     a.G = q_heads / kv_heads;
     a.D = head_dim;
     a.C = capacity;
-    a.R = a.Q * a.G;
-    a.chunk = chunk_slots(capacity);
-    a.chunks = static_cast<int>(ceil_div(capacity, a.chunk));
+    a.blocks = plan.blocks;
+    a.tile_rows = plan.tile_rows;
+    a.held_rows = plan.held_rows;
+    a.part = plan.part;
+    a.pitch = plan.pitch;
     a.scale2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634074);
     a.in = scores;
     a.out = out_scores;
     a.status = status;
-    a.part = reinterpret_cast<float2 *>(static_cast<char *>(workspace) + L.part);
-    a.lse = reinterpret_cast<float *>(static_cast<char *>(workspace) + L.lse);
-    return dtype == SPEC_BF16 ? launch_score<Bf16>(a, 1, stream) : launch_score<F32>(a, 0, stream);
+    return f32 ? launch_score<F32>(a, plan.smem, 0, stream) : launch_score<Bf16>(a, plan.smem, 1, stream);
 }

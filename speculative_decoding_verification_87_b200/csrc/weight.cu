@@ -64,6 +64,11 @@ struct ScoreArgs {
     const float *in;
     float *out;
     int32_t *status;
+    // many rows
+    int R;                 // Q * G
+    int chunks;            // chunks of `part` slots (statistics)
+    int slots;             // slots of a block (weights)
+    float2 *stats;         // [B][H][R][chunks]
 };
 
 // Filled slots and queries of request b; !ok: left as it was.
@@ -398,6 +403,298 @@ __global__ void __launch_bounds__(kScoreThreads, 2) k_score(const __grid_constan
     }
 }
 
+// --------------------------------------------------------- many rows (bf16)
+// Where a key head has many rows (a prompt's last queries, a verification with
+// wide groups) the products no longer fit shared memory and the exponentials
+// and the tensor pipe bound the step, not the keys.  Two kernels, no cluster
+// (16 blocks of one SM each fit only some of the processing clusters, and
+// eight would leave SMs idle):
+//   k_score_rows   a warp holds 16 * MR rows as A fragments, the keys stream
+//                  through shared memory as B fragments for all warps; the
+//                  running (max, sum) of a row stays in its four lanes;
+//   k_score_slots  a warp holds 32 slots as A fragments, the rows are B
+//                  fragments in shared memory; a slot's sum over the rows
+//                  stays in its four lanes.
+// tcgen05 accumulators were built and measured for this step: they would
+// halve its time, but drop what falls below the running sum at each of the
+// D / 16 steps, and the weights came out 6e-6 off (2-norm, against 3e-7 here)
+// on peaked keys; mma.sync keeps fp32 accuracy.
+constexpr int kManyRows = 128;     // rows of a row tile
+constexpr int kRowStages = 3;
+constexpr int kRowSlots = 64;      // slots of a stage for each group of warps
+
+// Slots [t0, t0 + slots) below `end` as B fragments (512 bytes per 8 slots
+// and 32 elements), asynchronously; the rest as zeros.
+__device__ __forceinline__ void copy_slots(const ScoreArgs &a, const uint16_t *keys, int t0, int slots, int end, uint4 *dst)
+{
+    const int nb = (a.D + 31) / 32, chunks = nb * 4;
+    for (int i = threadIdx.x; i < slots * chunks; i += blockDim.x) {
+        const int slot = i / chunks, c = i - slot * chunks;
+        const bool in = t0 + slot < end && c * 8 < a.D;
+        const uint16_t *from = in ? keys + (t0 + slot) * a.k_slot + c * 8 : keys;
+        const uint32_t at = static_cast<uint32_t>(
+            __cvta_generic_to_shared(dst + ((slot >> 3) * nb + (c >> 2)) * 32 + (slot & 7) * 4 + (c & 3)));
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(at), "l"(from), "r"(in ? 16 : 0) : "memory");
+    }
+}
+
+// Statistics of the rows of one tile over one chunk of slots: grid (chunk,
+// row tile, request and head).
+template <int NB, int MR>
+__global__ void __launch_bounds__(kScoreThreads, 2) k_score_rows(const __grid_constant__ ScoreArgs a)
+{
+    extern __shared__ __align__(16) unsigned char smem[];
+    uint4 *ring = reinterpret_cast<uint4 *>(smem);
+    __shared__ float2 stat[kScoreWarps][16 * MR];
+    const int64_t head = blockIdx.z;
+    const int b = static_cast<int>(head / a.H), h = static_cast<int>(head % a.H);
+    const Span sp = span_of(a, b);
+    const int rows = (sp.end - sp.begin) * a.G, r0 = blockIdx.y * kManyRows;
+    const int t_begin = blockIdx.x * a.part, t_end = min(sp.end, t_begin + a.part);
+    asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
+    if (!sp.ok || r0 >= rows || t_begin >= t_end) return;
+    const int nr = min(rows - r0, kManyRows), nb = (a.D + 31) / 32;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
+    const int wr = (min(a.R, kManyRows) + 16 * MR - 1) / (16 * MR);  // warps over the rows
+    const int groups = (blockDim.x >> 5) / wr;                          // groups of them over the slots
+    const int rw = (warp % wr) * 16 * MR, sg = warp / wr;
+    const auto *keys = static_cast<const uint16_t *>(a.k) + b * a.k_req + h * a.k_head;
+    const int stage_slots = kRowSlots * groups, stage = stage_slots / 8 * nb * 32;  // uint4
+    const int stages = (t_end - t_begin + stage_slots - 1) / stage_slots;
+    for (int s = 0; s < kRowStages - 1; ++s) {
+        if (s < stages) copy_slots(a, keys, t_begin + s * stage_slots, stage_slots, t_end, ring + s * stage);
+        asm volatile("cp.async.commit_group;\n" ::: "memory");
+    }
+    // this warp's rows: lane (g, t) holds rows g and g + 8 of each 16
+    uint4 q[MR][NB][2];
+    int last[MR][2];  // the last slot a row sees
+#pragma unroll
+    for (int i = 0; i < MR; ++i)
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            const int r = r0 + rw + 16 * i + g + 8 * half;
+            const int qi = r / a.G, x = r - qi * a.G;
+            last[i][half] = sp.begin + qi;
+            const auto *row = static_cast<const uint16_t *>(a.q) + b * a.q_req + qi * a.q_tok +
+                              (static_cast<int64_t>(h) * a.G + x) * a.q_head;
+#pragma unroll
+            for (int j = 0; j < NB; ++j) {
+                uint4 raw[1];
+                load8<Bf16>(row, r < rows ? 32 * j + 8 * t : a.D, a.D, raw);
+                q[i][j][half] = raw[0];
+            }
+        }
+    float m[MR][2], l[MR][2];  // of this lane's columns, m in units of log2
+#pragma unroll
+    for (int i = 0; i < MR; ++i) m[i][0] = m[i][1] = -INFINITY, l[i][0] = l[i][1] = 0.f;
+    const float sc = a.scale2;
+
+    for (int s = 0; s < stages; ++s) {
+        asm volatile("cp.async.wait_group %0;\n" ::"n"(kRowStages - 2) : "memory");
+        __syncthreads();
+        {
+            const int next = s + kRowStages - 1;
+            if (next < stages)
+                copy_slots(a, keys, t_begin + next * stage_slots, stage_slots, t_end, ring + next % kRowStages * stage);
+            asm volatile("cp.async.commit_group;\n" ::: "memory");
+        }
+        const int t0 = t_begin + s * stage_slots + sg * kRowSlots;
+        const uint4 *tile = ring + s % kRowStages * stage + sg * (kRowSlots / 8) * nb * 32 + lane;
+        if (rw >= nr || t0 >= t_end) continue;
+        const bool whole = t0 + kRowSlots <= min(t_end, sp.begin + 1);
+#pragma unroll 1
+        for (int n0 = 0; n0 < kRowSlots / 8; n0 += 4) {
+            float c[4][MR][4];
+#pragma unroll
+            for (int n = 0; n < 4; ++n)
+#pragma unroll
+                for (int i = 0; i < MR; ++i) c[n][i][0] = c[n][i][1] = c[n][i][2] = c[n][i][3] = 0.f;
+#pragma unroll
+            for (int j = 0; j < NB; ++j)
+                if (j < nb) {
+#pragma unroll
+                    for (int n = 0; n < 4; ++n) {
+                        const uint4 w = tile[((n0 + n) * nb + j) * 32];
+#pragma unroll
+                        for (int i = 0; i < MR; ++i) {
+                            const uint4 u = q[i][j][0], v = q[i][j][1];
+                            mma_bf16(c[n][i], u.x, v.x, u.y, v.y, w.x, w.y);
+                            mma_bf16(c[n][i], u.z, v.z, u.w, v.w, w.z, w.w);
+                        }
+                    }
+                }
+#pragma unroll
+            for (int i = 0; i < MR; ++i)
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    float x[8];
+#pragma unroll
+                    for (int n = 0; n < 4; ++n)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            // rounded, here and in k_score_slots alike: a fused
+                            // product would differ from L's by half a step of s
+                            x[2 * n + e] = __fmul_rn(c[n][i][2 * half + e], sc);
+                            const int slot = t0 + (n0 + n) * 8 + 2 * t + e;
+                            if (!whole && !(slot < t_end && slot <= last[i][half])) x[2 * n + e] = -INFINITY;
+                        }
+                    float top = x[0];
+#pragma unroll
+                    for (int e = 1; e < 8; ++e) top = fmaxf(top, x[e]);
+                    if (top > m[i][half]) {
+                        l[i][half] *= ex2_approx(m[i][half] - top);
+                        m[i][half] = top;
+                    }
+                    const float mm = m[i][half] == -INFINITY ? 0.f : m[i][half];
+                    float e0 = 0.f, e1 = 0.f;
+#pragma unroll
+                    for (int e = 0; e < 8; e += 2) {
+                        e0 += ex2_approx(x[e] - mm);
+                        e1 += ex2_approx(x[e + 1] - mm);
+                    }
+                    l[i][half] += e0 + e1;
+                }
+        }
+    }
+    asm volatile("cp.async.wait_group 0;\n" ::: "memory");
+#pragma unroll
+    for (int i = 0; i < MR; ++i)
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            float mm = m[i][half], ll = l[i][half];
+#pragma unroll
+            for (int o = 1; o < 4; o <<= 1) {
+                const float om = __shfl_xor_sync(kFull, mm, o), ol = __shfl_xor_sync(kFull, ll, o);
+                merge(mm, ll, om, ol);
+                if (ol != ol) ll = ol;
+            }
+            if (t == 0) stat[warp][16 * i + g + 8 * half] = make_float2(mm, ll);
+        }
+    __syncthreads();
+    for (int r = threadIdx.x; r < nr; r += blockDim.x) {
+        float mm = -INFINITY, ll = 0.f;
+        for (int x = 0; x < groups; ++x) {
+            const float2 y = stat[x * wr + r / (16 * MR)][r % (16 * MR)];
+            merge(mm, ll, y.x, y.y);
+            if (y.y != y.y) ll = y.y;
+        }
+        __stcg(a.stats + (head * a.R + r0 + r) * a.chunks + blockIdx.x, make_float2(mm, ll));
+    }
+}
+
+// The weights of one chunk of slots: grid (chunk, request and head).
+template <int NB>
+__global__ void __launch_bounds__(kScoreThreads, 2) k_score_slots(const __grid_constant__ ScoreArgs a)
+{
+    constexpr int kM = NB <= 4 ? 2 : 1;  // m-tiles of 16 slots a warp
+    extern __shared__ __align__(16) unsigned char smem[];
+    uint4 *sq = reinterpret_cast<uint4 *>(smem);
+    __shared__ float L[kManyRows];
+    const int64_t head = blockIdx.y;
+    const int b = static_cast<int>(head / a.H), h = static_cast<int>(head % a.H);
+    const Span sp = span_of(a, b);
+    if (!sp.ok) {
+        if (threadIdx.x == 0 && blockIdx.x == 0 && h == 0 && a.status) atomicOr(a.status, SPEC_STATUS_CAPACITY);
+        return;
+    }
+    const int rows = (sp.end - sp.begin) * a.G;
+    const int t_begin = blockIdx.x * a.slots, t_end = min(sp.end, t_begin + a.slots);
+    if (t_begin >= t_end) return;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3, nb = (a.D + 31) / 32;
+    const auto *keys = static_cast<const uint16_t *>(a.k) + b * a.k_req + h * a.k_head;
+    const float *in = a.in + head * a.C;
+    float *out = a.out + head * a.C;
+    const float sc = a.scale2;
+    const int chunks = (sp.end + a.part - 1) / a.part;
+    for (int r0 = 0; r0 < max(rows, 1); r0 += kManyRows) {
+        const int nr = min(rows - r0, kManyRows), tiles = (nr + 7) / 8;
+        __syncthreads();
+        stage_rows<Bf16, NB>(a, b, h, r0, rows, tiles, sq);
+        if (r0 == 0) asm volatile("griddepcontrol.wait;\n" ::: "memory");
+        // eight lanes a row merge the chunks' statistics
+        for (int i = threadIdx.x; i < tiles * 64; i += kScoreThreads) {
+            const int r = i >> 3;
+            float mm = -INFINITY, ll = 0.f;
+            if (r < nr)
+                for (int c = i & 7; c < chunks; c += 8) {
+                    const float2 y = __ldcg(a.stats + (head * a.R + r0 + r) * a.chunks + c);
+                    merge(mm, ll, y.x, y.y);
+                    if (y.y != y.y) ll = y.y;
+                }
+#pragma unroll
+            for (int o = 1; o < 8; o <<= 1) {
+                const float om = __shfl_xor_sync(kFull, mm, o), ol = __shfl_xor_sync(kFull, ll, o);
+                merge(mm, ll, om, ol);
+                if (ol != ol) ll = ol;
+            }
+            // a row that is none weighs nothing
+            if ((i & 7) == 0) L[r] = r < nr ? mm + log2f(ll) : INFINITY;
+        }
+        __syncthreads();
+        for (int t0 = t_begin + warp * 16 * kM; t0 < t_end; t0 += kScoreWarps * 16 * kM) {
+            uint4 k[kM][NB][2];
+            float old[kM][2], sum[kM][2];
+            int first[kM][2];  // the first row that sees the slot
+#pragma unroll
+            for (int i = 0; i < kM; ++i)
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    const int slot = t0 + 16 * i + g + 8 * half;
+                    const auto *row = keys + slot * a.k_slot;
+#pragma unroll
+                    for (int j = 0; j < NB; ++j) {
+                        uint4 raw[1];
+                        load8<Bf16>(row, slot < t_end ? 32 * j + 8 * t : a.D, a.D, raw);
+                        k[i][j][half] = raw[0];
+                    }
+                    old[i][half] = t != 0 || slot >= t_end ? 0.f : r0 > 0 ? out[slot] : slot < sp.begin ? in[slot] : 0.f;
+                    sum[i][half] = 0.f;
+                    first[i][half] = max(0, (slot - sp.begin) * a.G - r0);
+                }
+            const bool whole = t0 + 16 * kM <= sp.begin + 1;
+#pragma unroll 2
+            for (int n = 0; n < tiles; ++n) {
+                float c[kM][4];
+#pragma unroll
+                for (int i = 0; i < kM; ++i) c[i][0] = c[i][1] = c[i][2] = c[i][3] = 0.f;
+#pragma unroll
+                for (int j = 0; j < NB; ++j)
+                    if (j < nb) {
+                        const uint4 w = sq[(n * nb + j) * 32 + lane];
+#pragma unroll
+                        for (int i = 0; i < kM; ++i) {
+                            const uint4 u = k[i][j][0], v = k[i][j][1];
+                            mma_bf16(c[i], u.x, v.x, u.y, v.y, w.x, w.y);
+                            mma_bf16(c[i], u.z, v.z, u.w, v.w, w.z, w.w);
+                        }
+                    }
+                const float2 y = *reinterpret_cast<const float2 *>(&L[n * 8 + 2 * t]);
+#pragma unroll
+                for (int i = 0; i < kM; ++i)
+#pragma unroll
+                    for (int half = 0; half < 2; ++half) {
+                        float z0 = __fmul_rn(c[i][2 * half], sc) - y.x, z1 = __fmul_rn(c[i][2 * half + 1], sc) - y.y;
+                        if (!whole) {
+                            if (n * 8 + 2 * t < first[i][half]) z0 = -INFINITY;
+                            if (n * 8 + 2 * t + 1 < first[i][half]) z1 = -INFINITY;
+                        }
+                        sum[i][half] += ex2_approx(z0) + ex2_approx(z1);
+                    }
+            }
+#pragma unroll
+            for (int i = 0; i < kM; ++i)
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    float x = sum[i][half];
+                    x += __shfl_xor_sync(kFull, x, 1);
+                    x += __shfl_xor_sync(kFull, x, 2);
+                    const int slot = t0 + 16 * i + g + 8 * half;
+                    if (t == 0 && slot < t_end) out[slot] = old[i][half] + x;
+                }
+        }
+    }
+}
+
 constexpr size_t kScoreAlign = 256;
 int64_t ceil_div(int64_t x, int64_t y) { return (x + y - 1) / y; }
 
@@ -470,6 +767,71 @@ int launch_score(const ScoreArgs &a, size_t smem, int dtype_index, int nb_index,
     return SPEC_OK;
 }
 
+// Many rows: taken for bf16 from kManyMin rows a key head on.
+constexpr int kManyMin = 48;
+
+// Chunks of slots of the statistics step and slots of a block of the weights
+// step: about two blocks a SM for each, in whole stages.
+struct ManyPlan {
+    int part, chunks, slots;
+    size_t stats_bytes;
+};
+ManyPlan many_plan(int B, int H, int R, int C)
+{
+    ManyPlan p;
+    const int64_t heads = static_cast<int64_t>(B) * H, tiles = ceil_div(R, kManyRows);
+    const int64_t want = std::max<int64_t>(1, 2 * 148 / (heads * tiles));
+    p.part = static_cast<int>(ceil_div(ceil_div(C, want), 128) * 128);
+    p.chunks = static_cast<int>(ceil_div(C, p.part));
+    const int64_t blocks = std::max<int64_t>(1, 2 * 148 / heads);
+    p.slots = static_cast<int>(ceil_div(ceil_div(C, blocks), 256) * 256);
+    p.stats_bytes = sizeof(float2) * static_cast<size_t>(heads) * R * p.chunks;
+    return p;
+}
+bool many_rows(bool f32, int R) { return !f32 && R >= kManyMin; }
+
+bool g_many_attr[64][3];
+
+template <int NB, int MR>
+int launch_many(ScoreArgs a, int nb_index, cudaStream_t st)
+{
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return SPEC_ECUDA;
+    {
+        std::lock_guard<std::mutex> lock(g_score_mu);
+        if (!g_many_attr[dev][nb_index]) {
+            if (cudaFuncSetAttribute(k_score_rows<NB, MR>, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024 - 4096) !=
+                    cudaSuccess ||
+                cudaFuncSetAttribute(k_score_slots<NB>, cudaFuncAttributeMaxDynamicSharedMemorySize, 128 * 1024) !=
+                    cudaSuccess)
+                return SPEC_ECUDA;
+            g_many_attr[dev][nb_index] = true;
+        }
+    }
+    const int nb = (a.D + 31) / 32, top = std::min(a.R, kManyRows);
+    const int wr = static_cast<int>(ceil_div(top, 16 * MR)), groups = std::max(1, kScoreWarps / wr);
+    const size_t ring = static_cast<size_t>(kRowStages) * kRowSlots / 8 * groups * nb * 512;
+    const unsigned heads = static_cast<unsigned>(a.B * a.H);
+    k_score_rows<NB, MR><<<dim3(static_cast<unsigned>(a.chunks), static_cast<unsigned>(ceil_div(a.R, kManyRows)), heads),
+                           32 * wr * groups, ring, st>>>(a);
+    if (cudaGetLastError() != cudaSuccess) return SPEC_ECUDA;
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.gridDim = dim3(static_cast<unsigned>(ceil_div(a.C, a.slots)), heads);
+    cfg.blockDim = dim3(kScoreThreads);
+    cfg.dynamicSmemBytes = ceil_div(top, 8) * nb * 512;
+    cfg.stream = st;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaLaunchKernelEx(&cfg, k_score_slots<NB>, a) != cudaSuccess) {
+        (void)cudaGetLastError();
+        return SPEC_ECUDA;
+    }
+    return SPEC_OK;
+}
+
 template <class Tag>
 int launch_score(const ScoreArgs &a, size_t smem, int dtype_index, cudaStream_t st)
 {
@@ -487,7 +849,11 @@ extern "C" size_t spec_score_workspace_size(int batch, int queries, int q_heads,
 {
     if (batch < 0 || queries < 1 || kv_heads < 1 || q_heads < kv_heads || q_heads % kv_heads != 0 || capacity < 1)
         return 0;
-    return kScoreAlign;
+    // both types fit: the statistics of the kernels for many rows
+    const int64_t rows = static_cast<int64_t>(queries) * (q_heads / kv_heads);
+    if (rows < kManyMin || rows > INT_MAX) return kScoreAlign;
+    const size_t n = many_plan(batch > 0 ? batch : 1, kv_heads, static_cast<int>(rows), capacity).stats_bytes;
+    return std::max(kScoreAlign, (n + kScoreAlign - 1) / kScoreAlign * kScoreAlign);
 }
 
 extern "C" int spec_cache_score(const void *q, const void *k, spec_dtype_t dtype, int64_t q_request_stride,
@@ -519,7 +885,7 @@ extern "C" int spec_cache_score(const void *q, const void *k, spec_dtype_t dtype
     if (batch == 0) return SPEC_OK;
     if (!q || !k || !begin || !end || !scores || !out_scores) return SPEC_EINVAL;
     if (((reinterpret_cast<uintptr_t>(q) | reinterpret_cast<uintptr_t>(k)) & 15u) != 0) return SPEC_EALIGN;
-    if (!workspace || (reinterpret_cast<uintptr_t>(workspace) % kScoreAlign) != 0 || workspace_bytes < kScoreAlign)
+    if (!workspace || (reinterpret_cast<uintptr_t>(workspace) % kScoreAlign) != 0 || workspace_bytes < spec_score_workspace_size(batch, queries, q_heads, kv_heads, capacity))
         return SPEC_EWORKSPACE;
     const bool f32 = dtype == SPEC_F32;
     const ScorePlan plan =
@@ -552,5 +918,17 @@ extern "C" int spec_cache_score(const void *q, const void *k, spec_dtype_t dtype
     a.in = scores;
     a.out = out_scores;
     a.status = status;
+    a.R = a.Q * a.G;
+    if (many_rows(f32, a.R)) {
+        if (static_cast<int64_t>(batch) * kv_heads > 65535) return SPEC_EUNSUPPORTED;
+        const ManyPlan many = many_plan(batch, kv_heads, a.R, capacity);
+        a.part = many.part;
+        a.chunks = many.chunks;
+        a.slots = many.slots;
+        a.stats = static_cast<float2 *>(workspace);
+        if (head_dim <= 64) return launch_many<2, 2>(a, 0, stream);
+        if (head_dim <= 128) return launch_many<4, 2>(a, 1, stream);
+        return launch_many<8, 1>(a, 2, stream);
+    }
     return f32 ? launch_score<F32>(a, plan.smem, 0, stream) : launch_score<Bf16>(a, plan.smem, 1, stream);
 }

@@ -90,6 +90,33 @@ def test_score_scales(sv, dtype, scale):
     check_score(sv, q, k, [197, 100], [200, 102], s, scale)
 
 
+@pytest.mark.parametrize("B, Q, G, H, D, C, scale", [
+    (2, 40, 7, 1, 128, 1500, None), (3, 13, 4, 2, 112, 4000, None), (1, 128, 1, 2, 64, 1025, None),
+    (9, 12, 8, 4, 128, 700, None), (1, 49, 1, 1, 8, 49, None), (2, 32, 4, 1, 72, 300, -0.3), (1, 64, 2, 1, 128, 260, 0.0),
+    (1, 200, 2, 1, 32, 900, 2.0), (150, 16, 3, 1, 64, 40, None), (1, 6, 8, 1, 128, 20000, None),
+])
+def test_score_many_rows(sv, B, Q, G, H, D, C, scale):
+    q, k, s = make(B + 3 * Q + C, B, Q, G, H, D, C, torch.bfloat16)
+    r = np.random.RandomState(C + Q)
+    end = r.randint(min(Q, C), C + 1, B)
+    end[0] = C
+    count = np.array([min(e, r.randint(0, Q + 1)) for e in end])
+    count[0] = min(Q, C)
+    check_score(sv, q, k, end - count, end, s, scale, inplace=bool(B % 2), transpose=bool(Q % 2))
+
+
+def test_score_many_rows_nan_inf(sv):
+    q, k, s = make(8, 1, 20, 4, 3, 64, 400, torch.bfloat16)
+    k[0, 1, 150, 3] = float("nan")
+    q[0, 7, 9, 0] = float("inf")          # one row of head 2's group
+    k[0, 0, :, 5] = float(torch.finfo(torch.bfloat16).min)   # the lowest value everywhere: equal products
+    q[0, :, :4, 5] = 1.0
+    out = sv.spec_cache_score(q.cuda(), k.cuda(), ints([380]), ints([400]), s.cuda()).cpu()
+    assert torch.isfinite(out[0, 0]).all() and torch.isnan(out[0, 1]).all()
+    # the row of query 7 sees slots up to 387; later ones belong to other rows
+    assert torch.isnan(out[0, 2, :388]).all() and torch.isfinite(out[0, 2, 388:]).all()
+
+
 def test_score_strides(sv):
     # heads and tokens of q and k inside larger tensors, slots apart
     q, k, s = make(6, 2, 3, 2, 2, 64, 100, torch.bfloat16)

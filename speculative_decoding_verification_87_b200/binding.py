@@ -8,7 +8,7 @@ is no fallback.  If the library has not been built, the first call raises.
 
 Build it with ``python -m speculative_decoding_verification_87_b200.build``.
 """
-import contextlib
+import array
 import ctypes
 import os
 import threading
@@ -463,20 +463,44 @@ def spec_plug_tokens(in_tokens, out_tokens, accepted_len, next_tokens=None, seq_
 # on `stream` (a stream of that device; default: the device's current one).
 # What they allocate belongs to that stream.
 
-def _on(dev, stream):
-    """The context in which a call on `dev` runs."""
-    if stream is not None:
-        if stream.device != dev:
-            raise ValueError(f"stream is on {stream.device}, the tensors on {dev}")
-        return torch.cuda.stream(stream)
-    if dev.index == torch.cuda.current_device():
-        return contextlib.nullcontext()
-    return torch.cuda.device(dev)
+class _On:
+    """The context in which a call on `dev` runs; `handle` is its stream.
+    Leaves the current device and stream alone where they are the call's."""
+    __slots__ = ("handle", "outer")
+
+    def __init__(self, dev, stream):
+        self.outer = None
+        if stream is not None:
+            if stream.device != dev:
+                raise ValueError(f"stream is on {stream.device}, the tensors on {dev}")
+            self.outer, self.handle = torch.cuda.stream(stream), stream.cuda_stream
+        else:
+            if dev.index != torch.cuda.current_device():
+                self.outer = torch.cuda.device(dev)
+            # the handle alone: torch.cuda.current_stream() makes a Stream
+            # object for it, 2 us of a 10 us call
+            self.handle = torch._C._cuda_getCurrentRawStream(dev.index)
+
+    def __enter__(self):
+        if self.outer is not None:
+            self.outer.__enter__()
+        return self.handle
+
+    def __exit__(self, *error):
+        if self.outer is not None:
+            return self.outer.__exit__(*error)
 
 
-def _one_device(dev, **tensors):
-    for name, t in tensors.items():
-        if t is not None and t.device != dev:
+def _at(t):
+    """A tensor's address as ctypes takes it for a pointer argument."""
+    return None if t is None else t.data_ptr()
+
+
+def _one_device(dev, *named):
+    """(name, tensor or None) pairs: all on `dev`."""
+    i = dev.index
+    for name, t in named:
+        if t is not None and t.get_device() != i:
             raise ValueError(f"{name} is on {t.device}, not on {dev}")
 
 
@@ -506,7 +530,7 @@ def spec_beam_select(logits, scores, vocab, keep, temperature=1.0, finished=None
     _need_cuda("scores", scores, torch.float32, (B, W))
     if finished is not None:
         _need_cuda("finished", finished, torch.int32, (B, W))
-    with _on(dev, stream):
+    with _On(dev, stream) as handle:
         if out_scores is None:
             out_scores = torch.empty((B, keep), dtype=torch.float32, device=dev)
         if out_parents is None:
@@ -522,9 +546,9 @@ def spec_beam_select(logits, scores, vocab, keep, temperature=1.0, finished=None
             _need_cuda("out_finished", out_finished, torch.int32, (B, keep))
         if status is not None:
             _need_cuda("status", status, torch.int32)
-        _one_device(dev, scores=scores, finished=finished, out_scores=out_scores,
-                    out_parents=out_parents, out_tokens=out_tokens, out_finished=out_finished,
-                    status=status, workspace_buf=workspace_buf)
+        _one_device(dev, ("scores", scores), ("finished", finished), ("out_scores", out_scores),
+                    ("out_parents", out_parents), ("out_tokens", out_tokens), ("out_finished", out_finished),
+                    ("status", status), ("workspace_buf", workspace_buf))
         lib = load_library()
         code = _dtype_code(logits)
         ws = None
@@ -532,10 +556,10 @@ def spec_beam_select(logits, scores, vocab, keep, temperature=1.0, finished=None
             need = lib.spec_beam_workspace_size(B, W, vocab)
             ws = _scratch(need, workspace_buf, dev) if need else workspace_buf
         rc = lib.spec_beam_select(
-            _ptr(logits), code, stride, _ptr(scores), _ptr(finished), int(end_token), B, W, vocab,
-            float(temperature), keep, _ptr(out_scores), _ptr(out_parents), _ptr(out_tokens),
-            _ptr(out_finished), _ptr(status), _ptr(ws), 0 if ws is None else ws.numel(),
-            _stream(stream))
+            _at(logits), code, stride, _at(scores), _at(finished), int(end_token), B, W, vocab,
+            float(temperature), keep, _at(out_scores), _at(out_parents), _at(out_tokens),
+            _at(out_finished), _at(status), _at(ws), 0 if ws is None else ws.numel(),
+            handle)
     _check(rc, "spec_beam_select")
     return out_scores, out_parents, out_tokens, out_finished
 
@@ -562,12 +586,12 @@ def _state_layout(states, lead, axis):
     t = states[0]
     if t.dim() < lead or (axis is not None and not lead <= axis < t.dim()):
         raise ValueError("axis must be a dimension after the request's and the beam's")
+    if not t.is_cuda:
+        raise ValueError("the states must be CUDA tensors")
     e = t.element_size()
-    shape, stride = tuple(t.shape), tuple(t.stride())
-    for i, x in enumerate(states):
-        if not x.is_cuda:
-            raise ValueError(f"states[{i}] must be a CUDA tensor")
-        if x.device != t.device or x.dtype != t.dtype or tuple(x.shape) != shape or x.stride() != stride:
+    shape, stride, dtype, dev = t.shape, t.stride(), t.dtype, t.get_device()
+    for x in states:
+        if x.shape != shape or x.stride() != stride or x.dtype is not dtype or x.get_device() != dev:
             raise ValueError("the states must share device, dtype, shape and strides")
     inner = lead if axis is None else axis + 1
     whole = _one_stride(shape[inner:], stride[inner:])
@@ -585,7 +609,8 @@ def _state_layout(states, lead, axis):
 
 
 def _pointers(states):
-    return (ctypes.c_void_p * len(states))(*(t.data_ptr() for t in states))
+    """The states' addresses as an array of 64-bit integers."""
+    return array.array("Q", [t.data_ptr() for t in states])
 
 
 def spec_reorder_beams(states, parents, axis=None, begin=None, end=None, status=None, stream=None):
@@ -613,13 +638,14 @@ def spec_reorder_beams(states, parents, axis=None, begin=None, end=None, status=
             _need_cuda(name, t, torch.int32, (B,))
     if status is not None:
         _need_cuda("status", status, torch.int32)
-    _one_device(dev, parents=parents, begin=begin, end=end, status=status)
+    _one_device(dev, ("parents", parents), ("begin", begin), ("end", end), ("status", status))
     e = states[0].element_size()
-    with _on(dev, stream):
+    addresses = _pointers(states)
+    with _On(dev, stream) as handle:
         rc = load_library().spec_reorder_beams(
-            _pointers(states), len(states), states[0].stride(0) * e, states[0].stride(1) * e,
-            segments, seg_stride, unit, cap, _ptr(begin), _ptr(end), _ptr(parents), B, W, width,
-            _ptr(status), _stream(stream))
+            addresses.buffer_info()[0], len(states), states[0].stride(0) * e, states[0].stride(1) * e,
+            segments, seg_stride, unit, cap, _at(begin), _at(end), _at(parents), B, W, width,
+            _at(status), handle)
     _check(rc, "spec_reorder_beams")
     return states
 
@@ -642,17 +668,18 @@ def spec_commit_path(states, base, path, num_nodes, axis, out_lens=None, status=
             raise ValueError(f"path must have {states[0].shape[0]} rows, got {B}")
     if base is not None:
         _need_cuda("base", base, torch.int32, (B,))
-    with _on(dev, stream):
+    with _On(dev, stream) as handle:
         if out_lens is None:
             out_lens = torch.empty((B,), dtype=torch.int32, device=dev)
         _need_cuda("out_lens", out_lens, torch.int32, (B,))
         if status is not None:
             _need_cuda("status", status, torch.int32)
-        _one_device(dev, base=base, path=path, out_lens=out_lens, status=status)
+        _one_device(dev, ("base", base), ("path", path), ("out_lens", out_lens), ("status", status))
         step = states[0].stride(0) * states[0].element_size() if states else cap
+        addresses = _pointers(states)
         rc = load_library().spec_commit_path(
-            _pointers(states), len(states), step, segments, seg_stride, unit, cap, _ptr(base),
-            _ptr(path), B, int(num_nodes), width, _ptr(out_lens), _ptr(status), _stream(stream))
+            addresses.buffer_info()[0], len(states), step, segments, seg_stride, unit, cap, _at(base),
+            _at(path), B, int(num_nodes), width, _at(out_lens), _at(status), handle)
     _check(rc, "spec_commit_path")
     return out_lens
 
@@ -691,20 +718,20 @@ def spec_cache_score(q, k, begin, end, scores, scale=None, out_scores=None, stat
     _need_cuda("out_scores", out_scores, torch.float32, (B, H, cap))
     if status is not None:
         _need_cuda("status", status, torch.int32)
-    _one_device(dev, k=k, begin=begin, end=end, scores=scores, out_scores=out_scores, status=status,
-                workspace_buf=workspace_buf)
+    _one_device(dev, ("k", k), ("begin", begin), ("end", end), ("scores", scores), ("out_scores", out_scores), ("status", status),
+                ("workspace_buf", workspace_buf))
     scale = D ** -0.5 if scale is None else float(scale)
     lib = load_library()
-    with _on(dev, stream):
+    with _On(dev, stream) as handle:
         ws = None
         if B > 0:
             need = lib.spec_score_workspace_size(B, Q, Hq, H, cap)
             ws = _scratch(need, workspace_buf, dev) if need else workspace_buf
         rc = lib.spec_cache_score(
-            _ptr(q), _ptr(k), _dtype_code(q), q.stride(0), q.stride(1), q.stride(2), k.stride(0),
-            k.stride(1), k.stride(2), _ptr(begin), _ptr(end), B, Q, Hq, H, D, cap, scale,
-            _ptr(scores), _ptr(out_scores), _ptr(status), _ptr(ws),
-            0 if ws is None else ws.numel(), _stream(stream))
+            _at(q), _at(k), _dtype_code(q), q.stride(0), q.stride(1), q.stride(2), k.stride(0),
+            k.stride(1), k.stride(2), _at(begin), _at(end), B, Q, Hq, H, D, cap, scale,
+            _at(scores), _at(out_scores), _at(status), _at(ws),
+            0 if ws is None else ws.numel(), handle)
     _check(rc, "spec_cache_score")
     return out_scores
 
@@ -737,24 +764,24 @@ def spec_cache_evict(k, v, scores, positions, lens, budget, sinks=0, recent=0, o
         return t.stride(0) * e, t.stride(1) * e, t.stride(2) * e, t.shape[3] * e
 
     lib = load_library()
-    with _on(dev, stream):
+    with _On(dev, stream) as handle:
         if out_lens is None:
             out_lens = torch.empty((B,), dtype=torch.int32, device=dev)
         _need_cuda("out_lens", out_lens, torch.int32, (B,))
         if status is not None:
             _need_cuda("status", status, torch.int32)
-        _one_device(dev, v=v, scores=scores, positions=positions, lens=lens, out_scores=out_scores,
-                    out_positions=out_positions, out_lens=out_lens, status=status,
-                    workspace_buf=workspace_buf)
+        _one_device(dev, ("v", v), ("scores", scores), ("positions", positions), ("lens", lens), ("out_scores", out_scores),
+                    ("out_positions", out_positions), ("out_lens", out_lens), ("status", status),
+                    ("workspace_buf", workspace_buf))
         ws = None
         if B > 0:
             need = lib.spec_evict_workspace_size(B, H, cap, int(budget))
             ws = _scratch(need, workspace_buf, dev) if need else workspace_buf
         rc = lib.spec_cache_evict(
-            _ptr(k), _ptr(v), *layout(k), *(layout(v) if v is not None else (0, 0, 0, 0)),
-            _ptr(scores), _ptr(positions), _ptr(lens), B, H, cap, int(budget), int(sinks),
-            int(recent), _ptr(out_scores), _ptr(out_positions), _ptr(out_lens), _ptr(status),
-            _ptr(ws), 0 if ws is None else ws.numel(), _stream(stream))
+            _at(k), _at(v), *layout(k), *(layout(v) if v is not None else (0, 0, 0, 0)),
+            _at(scores), _at(positions), _at(lens), B, H, cap, int(budget), int(sinks),
+            int(recent), _at(out_scores), _at(out_positions), _at(out_lens), _at(status),
+            _at(ws), 0 if ws is None else ws.numel(), handle)
     _check(rc, "spec_cache_evict")
     return out_scores, out_positions, out_lens
 

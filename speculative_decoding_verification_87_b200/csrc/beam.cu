@@ -38,12 +38,15 @@ namespace {
 constexpr int kBeamThreads = 512;
 constexpr int kBeamWarps = kBeamThreads / 32;
 constexpr int kListMax = 256;  // items kept on the fast path
+constexpr unsigned kRehearse = 148;   // blocks that start while pass 1 streams
+constexpr int kHeldItems = 4096;     // item maxima kept in shared memory
+constexpr int kGroups = 128;   // maxima the threshold is taken from (SPEC_MAX_BEAMS at least)
 // Bound on |ln S - ln S_exact| for a row sum merged from pass-1 partials:
 // every term carries the exponential's 2^-22 and at most |z| 2^-23 ln 2 from
 // rounding log2(e)/T and z = (l - m) log2(e)/T, whose weighted mean is at most
 // log2 V bits (entropy), 1.5e-6 for V = 2^18; the sums of an item (17
-// additions deep, 2^-24 each) and the rescaling by fp32 exponentials 1.4e-6
-// and 1.2e-6 more.
+// additions deep, 2^-24 each), the rescaling by fp32 exponentials, the sum over
+// the items and the logarithm 1.4e-6, 1.2e-6, 4e-7 and 1e-7 more.
 constexpr double kBaseErr = 6e-6;
 
 struct BeamArgs {
@@ -74,114 +77,132 @@ __device__ __forceinline__ float order_value(uint32_t k)
     return __uint_as_float((k & 0x80000000u) ? k ^ 0x80000000u : ~k);
 }
 
+// ln s for a normal s > 0: exponent and fp32 logarithm of the mantissa in [1, 2),
+// within 1e-7 (an eighth of the fp64 logarithm's time on the critical path).
+__device__ __forceinline__ double log_fast(float s)
+{
+    const int u = __float_as_int(s);
+    const float m = __int_as_float((u & 0x7FFFFF) | 0x3F800000);
+    return static_cast<double>((u >> 23) - 127) * kLn2 + static_cast<double>(logf(m));
+}
+
 enum : int { kRowNone = 0, kRowLive = 1, kRowDone = 2 };
 
 struct BeamRows {
     double base[SPEC_MAX_BEAMS];  // scores - ln S
     double err[SPEC_MAX_BEAMS];   // bound on base's error
-    double s[SPEC_MAX_BEAMS];
+    float base32[SPEC_MAX_BEAMS];
     float m[SPEC_MAX_BEAMS];
-    int idx[SPEC_MAX_BEAMS];      // merge_row's argmax slot (unused here)
     float score[SPEC_MAX_BEAMS];
     int kind[SPEC_MAX_BEAMS];
     int exact[SPEC_MAX_BEAMS];    // 1: recompute wanted, 2: done
 };
 
 // Append the candidates of one item (row w, segment s) that reach lthr to
-// the list, at most `keep` of them: if more qualify, its `keep` best.  One
-// warp.  Returns through *count the list's new length, which may pass cap
-// (entries beyond it are not stored).
+// the list.  One warp.  *count is the list's new length, which may pass cap
+// (entries beyond it are not stored).  A vector's packed maximum decides
+// whether it is looked into; the few that are, are read again (L1), so that
+// the entries' code exists once: unrolled over the item it spent four times
+// as long, on instruction fetches.
 template <class Tag>
 __device__ __forceinline__ void gather_item(const Params &p, int b, int w, int s, float lthr, double base,
-                                            float m, int keep, Cand *cand, int cap, int *count)
+                                            float m, Cand *cand, int cap, int *count)
 {
     constexpr int kVec = Tag::kVec;
     constexpr int kV = Pass1Shape<Tag>::kVecL;
     constexpr int kEsz = sizeof(typename Tag::elem);
     const int lane = threadIdx.x & 31;
-    const int e0 = s * Pass1Shape<Tag>::kItem;
+    const int e0 = s * Pass1Shape<Tag>::kItem + lane * kVec;
     const char *row = static_cast<const char *>(p.tl) + (static_cast<int64_t>(b) * p.R + w) * p.stride * kEsz;
-    uint4 raw[kV];
+    auto vector = [&](int v) -> uint4 {
+        const int e = e0 + v * 32 * kVec;
+        return e < p.V ? mask_tail<Tag>(ldg_vec(row + static_cast<int64_t>(e) * kEsz), p.V - e)
+                       : make_uint4(Tag::kNegInfWord, Tag::kNegInfWord, Tag::kNegInfWord, Tag::kNegInfWord);
+    };
+    auto reaches = [&](uint4 raw) {
+        const float top = vec_max<Tag>(raw);
+        return top >= lthr && top > -INFINITY;
+    };
+    unsigned hit = 0;
+    if (s * Pass1Shape<Tag>::kItem + Pass1Shape<Tag>::kItem <= p.V) {
+        uint4 raw[kV];
 #pragma unroll
-    for (int v = 0; v < kV; ++v) {
-        const int e = e0 + (v * 32 + lane) * kVec;
-        raw[v] = e < p.V ? mask_tail<Tag>(ldg_vec(row + static_cast<int64_t>(e) * kEsz), p.V - e)
-                         : make_uint4(Tag::kNegInfWord, Tag::kNegInfWord, Tag::kNegInfWord, Tag::kNegInfWord);
+        for (int v = 0; v < kV; ++v) raw[v] = ldg_vec(row + static_cast<int64_t>(e0 + v * 32 * kVec) * kEsz);
+#pragma unroll
+        for (int v = 0; v < kV; ++v) hit |= reaches(raw[v]) ? 1u << v : 0u;
+    } else {
+#pragma unroll 1
+        for (int v = 0; v < kV; ++v) hit |= reaches(vector(v)) ? 1u << v : 0u;
     }
-    auto reaching = [&](float t) {  // entries >= t above -inf
+    for (unsigned todo = __reduce_or_sync(kFull, hit); todo; todo &= todo - 1) {
+        const int v = __ffs(todo) - 1;
+        float x[kVec];
+        unpack<Tag>(vector(v), x);
+        unsigned in = 0;
+#pragma unroll
+        for (int e = 0; e < kVec; ++e) in |= x[e] >= lthr && x[e] > -INFINITY ? 1u << e : 0u;
+        int incl = __popc(in);
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(kFull, incl, o);
+            if (lane >= o) incl += y;
+        }
+        int at = 0;
+        if (lane == 31) at = atomicAdd(count, incl);
+        at = __shfl_sync(kFull, at, 31) + incl - __popc(in);
+        for (; in; in &= in - 1, ++at) {
+            const int e = e0 + v * 32 * kVec + __ffs(in) - 1;
+            const float l = load_logit<Tag>(row, e);
+            if (at < cap) cand[at] = {base + (static_cast<double>(l) - static_cast<double>(m)) * p.inv_t, w, e};
+        }
+    }
+}
+
+// The `keep` best entries of one item, appended: those above the largest
+// value that `keep` entries reach, and of those equal to it the first in
+// index order.  One warp; for rows of many equal values.
+template <class Tag>
+__device__ __noinline__ void gather_best(const Params &p, int b, int w, int s, double base, float m, int keep,
+                                         Cand *cand, int cap, int *count)
+{
+    constexpr int kEsz = sizeof(typename Tag::elem);
+    const int lane = threadIdx.x & 31;
+    const int e0 = s * Pass1Shape<Tag>::kItem, n = min(p.V - e0, Pass1Shape<Tag>::kItem);
+    const int64_t row = (static_cast<int64_t>(b) * p.R + w) * p.stride + e0;
+    static_assert(kEsz == 2 || kEsz == 4, "bf16 or fp32");
+    auto reaching = [&](float t) {
         int c = 0;
-#pragma unroll
-        for (int v = 0; v < kV; ++v) {
-            float x[kVec];
-            unpack<Tag>(raw[v], x);
-#pragma unroll
-            for (int e = 0; e < kVec; ++e) c += (x[e] >= t && x[e] > -INFINITY) ? 1 : 0;
+        for (int i = lane; i < n; i += 32) {
+            const float x = load_logit<Tag>(p.tl, row + i);
+            c += x >= t && x > -INFINITY ? 1 : 0;
         }
         return __reduce_add_sync(kFull, c);
     };
-    int c = reaching(lthr);
-    if (c == 0) return;
-    float t = lthr;
-    int ties = INT_MAX;  // entries equal to t to take, in index order
-    if (c > keep) {
-        // the largest t that at least `keep` entries reach
-        uint32_t lo = order_key(lthr), hi = order_key(INFINITY);
-        while (lo < hi) {
-            const uint32_t mid = lo + (hi - lo + 1) / 2;
-            if (reaching(order_value(mid)) >= keep) lo = mid;
-            else hi = mid - 1;
-        }
-        t = order_value(lo);
-        int above = 0;
-#pragma unroll
-        for (int v = 0; v < kV; ++v) {
-            float x[kVec];
-            unpack<Tag>(raw[v], x);
-#pragma unroll
-            for (int e = 0; e < kVec; ++e) above += x[e] > t ? 1 : 0;
-        }
-        ties = keep - __reduce_add_sync(kFull, above);
-        c = keep;
+    uint32_t lo = order_key(-INFINITY), hi = order_key(INFINITY);
+    while (lo < hi) {
+        const uint32_t mid = lo + (hi - lo + 1) / 2;
+        if (reaching(order_value(mid)) >= keep) lo = mid;
+        else hi = mid - 1;
     }
+    const float t = order_value(lo);
+    const int all = reaching(t);
+    int above = 0;
+    for (int i = lane; i < n; i += 32) above += load_logit<Tag>(p.tl, row + i) > t ? 1 : 0;
+    int ties = min(all, keep) - __reduce_add_sync(kFull, above);  // entries equal to t to take
     int at = 0;
-    if (lane == 0) at = atomicAdd(count, c);
+    if (lane == 0) at = atomicAdd(count, min(all, keep));
     at = __shfl_sync(kFull, at, 0);
-#pragma unroll
-    for (int v = 0; v < kV; ++v) {
-        float x[kVec];
-        unpack<Tag>(raw[v], x);
-        int eq = 0, gt = 0;
-#pragma unroll
-        for (int e = 0; e < kVec; ++e) {
-            const bool in = x[e] >= t && x[e] > -INFINITY;
-            eq += in && x[e] == t ? 1 : 0;
-            gt += in && x[e] != t ? 1 : 0;
-        }
-        if (!__any_sync(kFull, (eq | gt) != 0)) continue;
-        // lane prefixes: an equal entry is taken while `ties` lasts
-        int peq = eq, pgt = gt;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int a = __shfl_up_sync(kFull, peq, o), g = __shfl_up_sync(kFull, pgt, o);
-            if (lane >= o) {
-                peq += a;
-                pgt += g;
-            }
-        }
-        const int teq = __shfl_sync(kFull, peq, 31), tgt = __shfl_sync(kFull, pgt, 31);
-        int seen = peq - eq;                         // equal entries of lower lanes
-        int slot = at + (pgt - gt) + min(seen, ties);
-#pragma unroll
-        for (int e = 0; e < kVec; ++e) {
-            if (!(x[e] >= t && x[e] > -INFINITY)) continue;
-            if (x[e] == t && seen++ >= ties) continue;
-            if (slot < cap)
-                cand[slot] = {base + (static_cast<double>(x[e]) - static_cast<double>(m)) * p.inv_t, w,
-                              e0 + (v * 32 + lane) * kVec + e};
-            ++slot;
-        }
-        at += tgt + min(teq, ties);
-        ties -= min(teq, ties);
+    for (int i0 = 0; i0 < n; i0 += 32) {
+        const int i = i0 + lane;
+        const float x = i < n ? load_logit<Tag>(p.tl, row + i) : -INFINITY;
+        const unsigned eq = __ballot_sync(kFull, x == t && x > -INFINITY);
+        const bool take = x > t || (x == t && x > -INFINITY && __popc(eq & ((1u << lane) - 1)) < ties);
+        const unsigned taken = __ballot_sync(kFull, take);
+        const int slot = at + __popc(taken & ((1u << lane) - 1));
+        if (take && slot < cap)
+            cand[slot] = {base + (static_cast<double>(x) - static_cast<double>(m)) * p.inv_t, w, e0 + i};
+        at += __popc(taken);
+        ties -= min(ties, __popc(eq));
     }
 }
 
@@ -225,179 +246,249 @@ __global__ void __launch_bounds__(kBeamThreads)
     __shared__ int list[kListMax];
     __shared__ int nlist, ncand, bad, again;
     __shared__ Cand warp_best[kBeamWarps];
+    __shared__ float thread_max[kBeamThreads];
+    __shared__ __align__(16) float group_max[kGroups];
+    __shared__ float held[kHeldItems];
+    __shared__ unsigned bound;
 
     const int b = blockIdx.x, W = p.R, S = p.S, K = a.keep;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    int kind = kRowNone;  // of row tid
     if (tid == 0) bad = 0;
-    __syncthreads();
     if (tid < W) {
         const float sc = __ldg(p.beam_scores + static_cast<int64_t>(b) * W + tid);
         const bool done = p.beam_done && __ldg(p.beam_done + static_cast<int64_t>(b) * W + tid) != 0;
+        kind = sc == -INFINITY ? kRowNone : done ? kRowDone : kRowLive;
         rw.score[tid] = sc;
-        rw.kind[tid] = sc == -INFINITY ? kRowNone : done ? kRowDone : kRowLive;
-        rw.exact[tid] = 0;
-        if (!(sc < INFINITY)) bad = 1;  // NaN or +inf
-    }
-    asm volatile("griddepcontrol.wait;\n" ::: "memory");
-    __syncthreads();
-    for (int w = warp; w < W; w += kBeamWarps)
-        if (rw.kind[w] == kRowLive) merge_row<kBeam>(p, b, w, RowStats{rw.s, rw.m, rw.idx});
-    __syncthreads();
-    if (tid < W && rw.kind[tid] == kRowLive) {
-        const float m = rw.m[tid];
-        if (m == -INFINITY) {
-            rw.kind[tid] = kRowNone;  // nothing to go on with
-        } else if (!stoch_row_ok(m, rw.s[tid])) {
-            bad = 1;
-        } else {
-            rw.base[tid] = static_cast<double>(rw.score[tid]) - log(rw.s[tid]);
-            rw.err[tid] = kBaseErr;
-        }
+        rw.kind[tid] = kind;
     }
     __syncthreads();
-    const int64_t o = static_cast<int64_t>(b) * K;
-    if (bad) {
-        if (tid < K) {
-            a.out_s[o + tid] = -INFINITY;
-            a.out_p[o + tid] = -1;
-            a.out_t[o + tid] = -1;
-            if (a.out_f) a.out_f[o + tid] = 0;
-        }
-        if (tid == 0) report(p.status, kStLogit);
-        return;
-    }
-
     const float2 *part = p.rowpart + static_cast<int64_t>(b) * W * S;
     const int items = W * S;
-    // score of item i's best candidate (-inf: none)
-    auto item_score = [&](int i) -> double {
-        const int w = i / S;
+    const float inv_t = static_cast<float>(p.inv_t);
+    // score of the best candidate of item s of row w (-inf: none), in fp32
+    auto item_key = [&](int w, int s) -> float {
+        const int i = w * S + s;
+        const float m = i < kHeldItems ? held[i] : __ldcg(&part[i].x);
+        return rw.kind[w] != kRowLive || m == -INFINITY ? -INFINITY : fmaf(m - rw.m[w], inv_t, rw.base32[w]);
+    };
+    // and in fp64
+    auto item_score = [&](int w, int s) -> double {
         if (rw.kind[w] != kRowLive) return -INFINITY;
-        const float m = __ldcg(&part[i].x);
+        const int i = w * S + s;
+        const float m = i < kHeldItems ? held[i] : __ldcg(&part[i].x);
         return m == -INFINITY ? -INFINITY
                               : rw.base[w] + (static_cast<double>(m) - static_cast<double>(rw.m[w])) * p.inv_t;
     };
+    // The steps run twice: a rehearsal while pass 1 still streams, over what the
+    // workspace happens to hold, then the real one.  The kernel is a chain of
+    // short steps, each of whose instructions came from L2 in a cold launch;
+    // the rehearsal fetches them (and the translations of the rows' pages) in
+    // time that is spent waiting anyway.  It writes nothing but shared memory.
+    // (Blocks past the first wave start when pass 1 is done: they skip it.)
+    const int64_t o = static_cast<int64_t>(b) * K;
     int found = 0;
-    for (;;) {
-        // a lower bound t0 of the K-th best candidate: the K-th largest of
-        // the threads' item maxima (each a candidate's score)
-        float mine = -INFINITY;
-        for (int i = tid; i < items; i += kBeamThreads) mine = fmaxf(mine, static_cast<float>(item_score(i)));
-        uint32_t lo = order_key(-INFINITY), hi = order_key(INFINITY);
-        const uint32_t key = order_key(mine);
-        while (lo < hi) {
-            const uint32_t mid = lo + (hi - lo + 1) / 2;
-            if (__syncthreads_count(key >= mid) >= K) lo = mid;
-            else hi = mid - 1;
-        }
-        const float t0f = order_value(lo);
-        // below t0 by the rounding of `mine` and the rows' errors, so that
-        // what the check below compares is in the list too
-        const double t0 = t0f == -INFINITY ? -INFINITY
-                                           : static_cast<double>(t0f) - (4.0 * kBaseErr + fabs(static_cast<double>(t0f)) * 2.4e-7);
-        if (tid == 0) {
-            nlist = 0;
-            ncand = 0;
-            again = 0;
-        }
-        __syncthreads();
-        for (int i = tid; i < items; i += kBeamThreads) {
-            const double s = item_score(i);
-            if (s >= t0 && s > -INFINITY) {
-                const int at = atomicAdd(&nlist, 1);
-                if (at < kListMax) list[at] = i;
+#pragma unroll 1
+    for (int run = blockIdx.x < kRehearse ? 0 : 1; run < 2; ++run) {
+        const bool real = run == 1;
+        if (real) {
+            __syncthreads();
+            if (tid < W) {
+                rw.kind[tid] = kind;
+                rw.exact[tid] = 0;
+                if (!(rw.score[tid] < INFINITY)) bad = 1;  // NaN or +inf
             }
+            asm volatile("griddepcontrol.wait;\n" ::: "memory");
+            __syncthreads();
         }
-        if (tid < W && rw.kind[tid] == kRowDone) {
-            const int at = atomicAdd(&ncand, 1);
-            cand[at] = {static_cast<double>(rw.score[tid]), tid, a.end_token};
-        }
-        __syncthreads();
-        bool whole = nlist <= kListMax;
-        auto gather = [&](int n) {
-            for (int j = warp; j < n; j += kBeamWarps) {
-                const int w = list[j] / S;
-                // the row's logits that may reach t0, rounded down
-                float lthr = -INFINITY;
-                if (t0 != -INFINITY) {
-                    const double l = static_cast<double>(rw.m[w]) + (t0 - rw.base[w]) / p.inv_t;
-                    lthr = static_cast<float>(l - fabs(l) * 1.2e-7);
+        // merge the rows, a warp each
+        for (int w = warp; w < W; w += kBeamWarps) {
+            if (rw.kind[w] != kRowLive) continue;
+            // the items' maxima (kept for the steps below) and the row's, then
+            // the sum of the items' sums brought to it
+            float m = -INFINITY, sum = 0.f;
+            for (int i = lane; i < S; i += 32) {
+                const float2 x = __ldcg(&part[w * S + i]);
+                if (w * S + i < kHeldItems) held[w * S + i] = x.x;
+                const float n = max_nan(m, x.x);
+                if (n == -INFINITY) continue;
+                sum = sum * ex2_approx((m - n) * p.c) + x.y * ex2_approx((x.x - n) * p.c);
+                m = n;
+            }
+            const float top = warp_max_nan(m);
+            sum = warp_sum(m == -INFINITY ? 0.f : sum * ex2_approx((m - top) * p.c));
+            if (lane == 0) {
+                rw.m[w] = top;
+                if (top == -INFINITY) {
+                    rw.kind[w] = kRowNone;  // nothing to go on with
+                } else if (!stoch_row_ok(top, sum)) {
+                    bad = 1;
+                } else {
+                    rw.base[w] = static_cast<double>(rw.score[w]) - log_fast(sum);
+                    rw.err[w] = kBaseErr;
+                    rw.base32[w] = static_cast<float>(rw.base[w]);
                 }
-                gather_item<Tag>(p, b, w, list[j] - w * S, lthr, rw.base[w], rw.m[w], K, cand, a.cap, &ncand);
             }
-        };
-        if (whole) {
-            gather(nlist);
-            __syncthreads();
-            whole = ncand <= a.cap;
+            __syncwarp();
         }
-        if (!whole) {
-            // many equal maxima: exactly the K best items, one by one
-            int n = 0;
-            Cand last = {INFINITY, -1, -1};
-            __syncthreads();
-            if (tid == 0) ncand = 0;
-            __syncthreads();
-            if (tid < W && rw.kind[tid] == kRowDone) {
-                const int at = atomicAdd(&ncand, 1);
-                cand[at] = {static_cast<double>(rw.score[tid]), tid, a.end_token};
+        __syncthreads();
+        if (!real) bad = 0;  // every thread: what stale partials say is nothing
+        __syncthreads();
+        if (bad) {
+            if (tid < K) {
+                a.out_s[o + tid] = -INFINITY;
+                a.out_p[o + tid] = -1;
+                a.out_t[o + tid] = -1;
+                if (a.out_f) a.out_f[o + tid] = 0;
             }
-            for (; n < min(K, kListMax); ++n) {
-                Cand top = {-INFINITY, INT_MAX, INT_MAX};
-                for (int i = tid; i < items; i += kBeamThreads) {
-                    const Cand c = {item_score(i), i / S, i - (i / S) * S};
-                    if (c.s > -INFINITY && better(last, c) && better(c, top)) top = c;
+            if (tid == 0) report(p.status, kStLogit);
+            return;
+        }
+
+        for (;;) {
+            // a lower bound t0 of the K-th best candidate: the K-th largest of
+            // kGroups maxima of distinct items (each a candidate's score)
+            float mine = -INFINITY;
+            for (int w = warp; w < W; w += kBeamWarps)
+                for (int i = lane; i < S; i += 32) mine = fmaxf(mine, item_key(w, i));
+            thread_max[tid] = mine;
+            if (tid == 0) {
+                nlist = 0;
+                ncand = 0;
+                again = 0;
+                bound = 0xFFFFFFFFu;
+            }
+            __syncthreads();
+            // groups of threads of different warps, so of different rows where
+            // rows are many: the best row's best items stay apart
+            if (tid < kGroups) {
+    #pragma unroll
+                for (int x = kGroups; x < kBeamThreads; x += kGroups) mine = fmaxf(mine, thread_max[tid + x]);
+                group_max[tid] = mine;
+            }
+            __syncthreads();
+            {
+                // how many of the groups' maxima are larger, four threads a group:
+                // the least of those with fewer than K is the K-th largest
+                constexpr int kShare = kBeamThreads / kGroups;
+                const int j0 = tid % kShare * (kGroups / kShare);
+                const float x = group_max[tid / kShare];
+                int above = 0;
+#pragma unroll
+                for (int j = j0; j < j0 + kGroups / kShare; j += 4) {
+                    const float4 y = *reinterpret_cast<const float4 *>(&group_max[j]);
+                    above += (y.x > x ? 1 : 0) + (y.y > x ? 1 : 0) + (y.z > x ? 1 : 0) + (y.w > x ? 1 : 0);
                 }
 #pragma unroll
-                for (int x = 16; x > 0; x >>= 1) {
-                    const Cand c = {__shfl_xor_sync(kFull, top.s, x), __shfl_xor_sync(kFull, top.w, x),
-                                    __shfl_xor_sync(kFull, top.v, x)};
-                    if (better(c, top)) top = c;
+                for (int o = 1; o < kShare; o <<= 1) above += __shfl_xor_sync(kFull, above, o);
+                const uint32_t least = __reduce_min_sync(kFull, above < K ? order_key(x) : 0xFFFFFFFFu);
+                if (lane == 0) atomicMin(&bound, least);
+            }
+            __syncthreads();
+            const float t0f = order_value(bound);
+            // below t0 by the rows' errors, so that what the check below
+            // compares is in the list too; and by the keys' rounding, at most
+            // 4 steps of what adds up to a key
+            const double t0 = t0f == -INFINITY ? -INFINITY : static_cast<double>(t0f) - 4.0 * kBaseErr;
+            auto slack = [&](int w) { return 4.8e-7f * (fabsf(t0f) + fabsf(rw.base32[w])); };
+            for (int w = warp; w < W; w += kBeamWarps) {
+                const float least = t0f == -INFINITY ? -INFINITY : static_cast<float>(t0) - 2.f * slack(w);
+                for (int i = lane; i < S; i += 32) {
+                    const float key = item_key(w, i);
+                    if (key >= least && key > -INFINITY) {
+                        const int at = atomicAdd(&nlist, 1);
+                        if (at < kListMax) list[at] = w * S + i;
+                    }
                 }
-                if (lane == 0) warp_best[warp] = top;
+            }
+            auto add_done = [&]() {
+                if (tid < W && rw.kind[tid] == kRowDone)
+                    cand[atomicAdd(&ncand, 1)] = {static_cast<double>(rw.score[tid]), tid, a.end_token};
+            };
+            add_done();
+            __syncthreads();
+            bool whole = nlist <= kListMax;
+            if (whole) {
+                for (int j = warp; j < (real ? nlist : min(nlist, kBeamWarps)); j += kBeamWarps) {
+                    const int w = list[j] / S;
+                    // the row's logits that may reach t0, rounded down
+                    float lthr = -INFINITY;
+                    if (t0 != -INFINITY) {
+                        const double l = static_cast<double>(rw.m[w]) + (t0 - 2.f * slack(w) - rw.base[w]) / p.inv_t;
+                        lthr = static_cast<float>(l - fabs(l) * 1.2e-7);
+                    }
+                    gather_item<Tag>(p, b, w, list[j] - w * S, lthr, rw.base[w], rw.m[w], cand, a.cap, &ncand);
+                }
                 __syncthreads();
-                top = warp_best[0];
-                for (int i = 1; i < kBeamWarps; ++i)
-                    if (better(warp_best[i], top)) top = warp_best[i];
+                whole = ncand <= a.cap;
+            }
+            if (!whole && real) {
+                // many equal maxima: exactly the K best items, one by one, and of
+                // each its K best entries (K * K fit the list)
+                int n = 0;
+                Cand last = {INFINITY, -1, -1};
                 __syncthreads();
-                if (top.s == -INFINITY) break;
-                if (tid == 0) list[n] = top.w * S + top.v;
-                last = top;
+                if (tid == 0) ncand = 0;
+                __syncthreads();
+                add_done();
+                for (; n < K; ++n) {
+                    Cand top = {-INFINITY, INT_MAX, INT_MAX};
+                    for (int i = tid; i < items; i += kBeamThreads) {
+                        const Cand c = {item_score(i / S, i % S), i / S, i % S};
+                        if (c.s > -INFINITY && better(last, c) && better(c, top)) top = c;
+                    }
+    #pragma unroll
+                    for (int x = 16; x > 0; x >>= 1) {
+                        const Cand c = {__shfl_xor_sync(kFull, top.s, x), __shfl_xor_sync(kFull, top.w, x),
+                                        __shfl_xor_sync(kFull, top.v, x)};
+                        if (better(c, top)) top = c;
+                    }
+                    if (lane == 0) warp_best[warp] = top;
+                    __syncthreads();
+                    top = warp_best[0];
+                    for (int i = 1; i < kBeamWarps; ++i)
+                        if (better(warp_best[i], top)) top = warp_best[i];
+                    __syncthreads();
+                    if (top.s == -INFINITY) break;
+                    if (tid == 0) list[n] = top.w * S + top.v;
+                    last = top;
+                }
+                __syncthreads();
+                for (int j = warp; j < n; j += kBeamWarps) {
+                    const int w = list[j] / S;
+                    gather_best<Tag>(p, b, w, list[j] - w * S, rw.base[w], rw.m[w], K, cand, a.cap, &ncand);
+                }
+                if (tid == 0) nlist = n;
             }
             __syncthreads();
-            gather(n);  // at most K candidates an item: they fit
-            __syncthreads();
-            if (tid == 0) nlist = n;
-        }
-        __syncthreads();
 
-        // rank every candidate; the first K are the selection
-        const int n = ncand;
-        found = min(n, K);
-        for (int i = tid; i < n; i += kBeamThreads) {
-            const Cand c = cand[i];
-            int rank = 0;
-            for (int j = 0; j < n && rank < K; ++j) rank += better(cand[j], c) ? 1 : 0;
-            if (rank < K) best[rank] = c;
-        }
-        __syncthreads();
-        // rows whose errors could change it
-        auto err = [&](int w) { return rw.kind[w] == kRowLive ? rw.err[w] : 0.0; };
-        auto close = [&](const Cand &x, double s, int w) {
-            const double e = err(x.w) + err(w);
-            return w != x.w && e > 0.0 && fabs(x.s - s) <= e;
-        };
-        auto want = [&](int w) {
-            if (rw.kind[w] == kRowLive && rw.err[w] > 0.0) {
-                rw.exact[w] = 1;
-                again = 1;
+            // rank every candidate, a warp each; the first K are the selection
+            const int n = real ? ncand : min(ncand, kBeamWarps);
+            found = min(n, K);
+            for (int i = warp; i < n; i += kBeamWarps) {
+                const Cand c = cand[i];
+                int rank = 0;
+                for (int j = lane; j < n; j += 32) rank += better(cand[j], c) ? 1 : 0;
+                rank = __reduce_add_sync(kFull, rank);
+                if (lane == 0 && rank < K) best[rank] = c;
             }
-        };
-        if (tid + 1 < found && close(best[tid], best[tid + 1].s, best[tid + 1].w)) {
-            want(best[tid].w);
-            want(best[tid + 1].w);
-        }
-        if (n > K || nlist > 0) {
+            __syncthreads();
+            // rows whose errors could change it
+            auto err = [&](int w) { return rw.kind[w] == kRowLive ? rw.err[w] : 0.0; };
+            auto close = [&](const Cand &x, double s, int w) {
+                const double e = err(x.w) + err(w);
+                return w != x.w && e > 0.0 && fabs(x.s - s) <= e;
+            };
+            auto want = [&](int w) {
+                if (rw.kind[w] == kRowLive && rw.err[w] > 0.0) {
+                    rw.exact[w] = 1;
+                    again = 1;
+                }
+            };
+            if (tid + 1 < found && close(best[tid], best[tid + 1].s, best[tid + 1].w)) {
+                want(best[tid].w);
+                want(best[tid + 1].w);
+            }
             if (found == K) {
                 const Cand kth = best[K - 1];
                 for (int i = tid; i < n; i += kBeamThreads) {
@@ -407,34 +498,37 @@ __global__ void __launch_bounds__(kBeamThreads)
                         want(c.w);
                     }
                 }
-                // items that are not in the list (their maxima)
-                for (int i = tid; i < items; i += kBeamThreads) {
-                    const double s = item_score(i);
-                    const int w = i / S;
-                    if (s == -INFINITY || !close(kth, s, w)) continue;
-                    bool in = false;
-                    for (int j = 0; j < nlist && !in; ++j) in = list[j] == i;
-                    if (!in) {
-                        want(kth.w);
-                        want(w);
+                // items that are not in the list, by their maxima (a whole list
+                // leaves out only what lies further below)
+                if (!whole && real)
+                    for (int i = tid; i < items; i += kBeamThreads) {
+                        const int w = i / S;
+                        const double s = item_score(w, i % S);
+                        if (s == -INFINITY || !close(kth, s, w)) continue;
+                        bool in = false;
+                        for (int j = 0; j < nlist && !in; ++j) in = list[j] == i;
+                        if (!in) {
+                            want(kth.w);
+                            want(w);
+                        }
                     }
+            }
+            __syncthreads();
+            if (!again || !real) break;
+            for (int j = tid; j < kExp2Tab; j += kBeamThreads) tab[j] = p.exp2tab[j];
+            __syncthreads();
+            for (int w = 0; w < W; ++w) {
+                if (rw.exact[w] != 1) continue;
+                const double sum = exact_sum<Tag>(p, b, w, rw.m[w], tab, scratch);
+                if (tid == 0) {
+                    rw.base[w] = static_cast<double>(rw.score[w]) - log(sum);
+                    rw.base32[w] = static_cast<float>(rw.base[w]);
+                    rw.err[w] = 0.0;
+                    rw.exact[w] = 2;
                 }
             }
+            __syncthreads();
         }
-        __syncthreads();
-        if (!again) break;
-        for (int j = tid; j < kExp2Tab; j += kBeamThreads) tab[j] = p.exp2tab[j];
-        __syncthreads();
-        for (int w = 0; w < W; ++w) {
-            if (rw.exact[w] != 1) continue;
-            const double sum = exact_sum<Tag>(p, b, w, rw.m[w], tab, scratch);
-            if (tid == 0) {
-                rw.base[w] = static_cast<double>(rw.score[w]) - log(sum);
-                rw.err[w] = 0.0;
-                rw.exact[w] = 2;
-            }
-        }
-        __syncthreads();
     }
     if (tid < K) {
         const bool in = tid < found;
@@ -448,8 +542,8 @@ __global__ void __launch_bounds__(kBeamThreads)
 constexpr size_t kBeamAlign = 256;
 int64_t ceil_div(int64_t x, int64_t y) { return (x + y - 1) / y; }
 
-// counters (one claim counter), then the pass-1 partials [B][W][S] (S of the
-// shorter fp32 items, so that both dtypes fit)
+// pass 1's claim counter (touched, not used), then the pass-1 partials
+// [B][W][S] (S of the shorter fp32 items, so that both dtypes fit)
 size_t beam_bytes(int B, int W, int V)
 {
     if (B < 0 || W < 1 || W > SPEC_MAX_BEAMS || V < 1) return 0;
@@ -498,9 +592,11 @@ int launch_beam(Params &p, BeamArgs &a, int dtype_index, cudaStream_t st)
     }
     const int64_t blocks =
         std::max<int64_t>(1, std::min<int64_t>(static_cast<int64_t>(per_sm) * sms, ceil_div(p.nA, kWarps)));
-    const uint64_t warps = static_cast<uint64_t>(blocks) * kWarps;
-    p.nAs = static_cast<unsigned>((static_cast<uint64_t>(p.nA) * 88 / 100) / warps * warps);
-    if (cudaMemsetAsync(p.a_claim, 0xFF, sizeof(unsigned), st) != cudaSuccess) return SPEC_ECUDA;
+    // All items are static: the claimed tail of the other calls comes in
+    // chunks of four items and clearing its counter is a launch of its own
+    // (rows of 128256 bf16: 32 x 16 42.7 us static, 48.7 with a claimed tail;
+    // 128 x 16 139.5 and 143.1; 256 x 4 65.8 and 70.5)
+    p.nAs = p.nA;
     k_pass1<Tag, kBeam, 2><<<static_cast<unsigned>(blocks), kThreads, kRingBytes, st>>>(p);
     if (cudaGetLastError() != cudaSuccess) return SPEC_ECUDA;
     a.cap = static_cast<int>(cand_count(a.keep));

@@ -64,11 +64,12 @@ struct ScoreArgs {
     const float *in;
     float *out;
     int32_t *status;
-    // many rows
+    // few and many rows
     int R;                 // Q * G
     int chunks;            // chunks of `part` slots (statistics)
-    int slots;             // slots of a block (weights)
+    int slots;             // slots of a block (weights), of a warp's stage (statistics)
     float2 *stats;         // [B][H][R][chunks]
+    float *held;           // few rows: products [B][H][R][pitch]
 };
 
 // Filled slots and queries of request b; !ok: left as it was.
@@ -213,7 +214,7 @@ __device__ __forceinline__ void stage_rows(const ScoreArgs &a, int b, int h, int
 
 // The products of a warp's 16 slots with n-tiles [tile0, tile0 + kGroup):
 // fp32 accumulators, c[n][0..1] slot g rows 2t, 2t+1; c[n][2..3] slot g + 8.
-template <class Tag, int NB>
+template <class Tag, int NB, int kGroup>
 __device__ __forceinline__ void products(const Slots<Tag, NB> &k, const uint4 *sq, int nb, int tile0, int tiles,
                                          float (&c)[kGroup][4])
 {
@@ -301,7 +302,7 @@ __global__ void __launch_bounds__(kScoreThreads, 2) k_score(const __grid_constan
                 const int g = lane >> 2, t2 = 2 * (lane & 3);
                 for (int tile0 = 0; tile0 < tiles; tile0 += kGroup) {
                     float c[kGroup][4];
-                    products<Tag, NB>(cur, sq, nb, tile0, tiles, c);
+                    products<Tag, NB, kGroup>(cur, sq, nb, tile0, tiles, c);
 #pragma unroll
                     for (int n = 0; n < kGroup; ++n) {
 #pragma unroll
@@ -403,6 +404,144 @@ __global__ void __launch_bounds__(kScoreThreads, 2) k_score(const __grid_constan
     }
 }
 
+// ------------------------------------------------------------------ few rows
+// Decoding and small verifications: reading the keys bounds the step, so they
+// are read once.  k_score_few forms the products, stores them and the
+// statistics of its chunk; k_score_sum merges the statistics and adds up the
+// weights from the stored products.  They are written and read once, 8 bytes
+// per product, which is less than a second read of the keys while
+// 8 R < D * element size.  No cluster, no wait: a head of any length spreads
+// over the whole GPU.
+constexpr int kFewRows = 32;
+
+// Products and statistics of one chunk of slots: grid (chunk, head).  A warp
+// takes every eighth 16 slots of the chunk, the next ones in flight; the
+// running (max, sum) of a row stays in the lanes that hold its column.
+template <class Tag, int NB, int NT>
+__global__ void __launch_bounds__(kScoreThreads, 2) k_score_few(const __grid_constant__ ScoreArgs a)
+{
+    extern __shared__ __align__(16) unsigned char smem[];
+    uint4 *sq = reinterpret_cast<uint4 *>(smem);
+    __shared__ float2 stat[kScoreWarps][8 * NT];
+    const int64_t head = blockIdx.y;
+    const int b = static_cast<int>(head / a.H), h = static_cast<int>(head % a.H);
+    const Span sp = span_of(a, b);
+    asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
+    const int rows = (sp.end - sp.begin) * a.G;
+    const int t_begin = blockIdx.x * a.part, t_end = min(sp.end, t_begin + a.part);
+    if (!sp.ok || rows == 0 || t_begin >= t_end) return;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t2 = 2 * (lane & 3);
+    const int nb = (a.D + 31) / 32, tiles = (rows + 7) / 8;
+    const auto *keys = static_cast<const typename Tag::elem *>(a.k) + b * a.k_req + h * a.k_head;
+    float *products_out = a.held + head * a.R * a.pitch;
+    Slots<Tag, NB> cur, next;
+    int t0 = t_begin + warp * 16;
+    if (t0 < t_end) cur.load(a, keys, t0, t_end);
+    stage_rows<Tag, NB>(a, b, h, 0, rows, tiles, sq);
+    __syncthreads();
+    float m[NT][2], l[NT][2];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) m[n][0] = m[n][1] = -INFINITY, l[n][0] = l[n][1] = 0.f;
+    for (; t0 < t_end; t0 += kScoreWarps * 16) {
+        if (t0 + kScoreWarps * 16 < t_end) next.load(a, keys, t0 + kScoreWarps * 16, t_end);
+        float c[NT][4];
+        products<Tag, NB, NT>(cur, sq, nb, 0, tiles, c);
+        const bool whole = t0 + 16 <= min(t_end, sp.begin + 1);
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int r = n * 8 + t2 + e;
+                if (r < rows) {
+                    float x[2];
+#pragma unroll
+                    for (int half = 0; half < 2; ++half) {
+                        const int t = t0 + g + 8 * half;
+                        x[half] = __fmul_rn(c[n][2 * half + e], a.scale2);
+                        if (!whole && !(t < t_end && t <= sp.begin + r / a.G)) x[half] = -INFINITY;
+                        if (whole || t < t_end) products_out[static_cast<int64_t>(r) * a.pitch + t] = x[half];
+                    }
+                    const float top = fmaxf(x[0], x[1]);
+                    if (top > m[n][e]) {
+                        l[n][e] *= ex2_approx(m[n][e] - top);
+                        m[n][e] = top;
+                    }
+                    const float mm = m[n][e] == -INFINITY ? 0.f : m[n][e];
+                    l[n][e] += ex2_approx(x[0] - mm) + ex2_approx(x[1] - mm);
+                }
+            }
+        cur = next;
+    }
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            float mm = m[n][e], ll = l[n][e];
+#pragma unroll
+            for (int o = 4; o < 32; o <<= 1) {
+                const float om = __shfl_xor_sync(kFull, mm, o), ol = __shfl_xor_sync(kFull, ll, o);
+                merge(mm, ll, om, ol);
+                if (ol != ol) ll = ol;
+            }
+            if (g == 0) stat[warp][n * 8 + t2 + e] = make_float2(mm, ll);
+        }
+    __syncthreads();
+    if (threadIdx.x < rows) {
+        float mm = -INFINITY, ll = 0.f;
+        for (int w = 0; w < kScoreWarps; ++w) {
+            const float2 y = stat[w][threadIdx.x];
+            merge(mm, ll, y.x, y.y);
+            if (y.y != y.y) ll = y.y;
+        }
+        __stcg(a.stats + (head * a.R + threadIdx.x) * a.chunks + blockIdx.x, make_float2(mm, ll));
+    }
+}
+
+// The weights of 256 slots: grid (slots, head), a thread each.
+__global__ void __launch_bounds__(kScoreThreads) k_score_sum(const __grid_constant__ ScoreArgs a)
+{
+    __shared__ float L[kFewRows];
+    const int64_t head = blockIdx.y;
+    const int b = static_cast<int>(head / a.H);
+    const Span sp = span_of(a, b);
+    if (!sp.ok) {
+        if (threadIdx.x == 0 && blockIdx.x == 0 && head % a.H == 0 && a.status) atomicOr(a.status, SPEC_STATUS_CAPACITY);
+        return;
+    }
+    const int rows = (sp.end - sp.begin) * a.G, t_begin = blockIdx.x * kScoreThreads;
+    if (t_begin >= sp.end) return;
+    const int t = t_begin + threadIdx.x;
+    float *out = a.out + head * a.C;
+    const float old = t < sp.begin ? a.in[head * a.C + t] : 0.f;
+    const int chunks = (sp.end + a.part - 1) / a.part;
+    asm volatile("griddepcontrol.wait;\n" ::: "memory");
+    {  // eight lanes a row merge the chunks' statistics
+        const int r = threadIdx.x >> 3;
+        float mm = -INFINITY, ll = 0.f;
+        if (r < rows)
+            for (int c = threadIdx.x & 7; c < chunks; c += 8) {
+                const float2 y = __ldcg(a.stats + (head * a.R + r) * a.chunks + c);
+                merge(mm, ll, y.x, y.y);
+                if (y.y != y.y) ll = y.y;
+            }
+#pragma unroll
+        for (int o = 1; o < 8; o <<= 1) {
+            const float om = __shfl_xor_sync(kFull, mm, o), ol = __shfl_xor_sync(kFull, ll, o);
+            merge(mm, ll, om, ol);
+            if (ol != ol) ll = ol;
+        }
+        if ((threadIdx.x & 7) == 0) L[r] = mm + log2f(ll);
+    }
+    __syncthreads();
+    if (t >= sp.end) return;
+    const float *s = a.held + head * a.R * a.pitch + t;
+    float sum = 0.f;
+#pragma unroll 8
+    for (int r = max(0, (t - sp.begin) * a.G); r < rows; ++r)  // the rows that see the slot
+        sum += ex2_approx(__ldcg(s + static_cast<int64_t>(r) * a.pitch) - L[r]);
+    out[t] = old + sum;
+}
+
 // --------------------------------------------------------- many rows (bf16)
 // Where a key head has many rows (a prompt's last queries, a verification with
 // wide groups) the products no longer fit shared memory and the exponentials
@@ -421,7 +560,6 @@ __global__ void __launch_bounds__(kScoreThreads, 2) k_score(const __grid_constan
 // on peaked keys; mma.sync keeps fp32 accuracy.
 constexpr int kManyRows = 128;     // rows of a row tile
 constexpr int kRowStages = 3;
-constexpr int kRowSlots = 64;      // slots of a stage for each group of warps
 
 // Slots [t0, t0 + slots) below `end` as B fragments (512 bytes per 8 slots
 // and 32 elements), asynchronously; the rest as zeros.
@@ -457,9 +595,10 @@ __global__ void __launch_bounds__(kScoreThreads, 2) k_score_rows(const __grid_co
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
     const int wr = (min(a.R, kManyRows) + 16 * MR - 1) / (16 * MR);  // warps over the rows
     const int groups = (blockDim.x >> 5) / wr;                          // groups of them over the slots
+    const int row_slots = a.slots;                                      // of a stage, for each group
     const int rw = (warp % wr) * 16 * MR, sg = warp / wr;
     const auto *keys = static_cast<const uint16_t *>(a.k) + b * a.k_req + h * a.k_head;
-    const int stage_slots = kRowSlots * groups, stage = stage_slots / 8 * nb * 32;  // uint4
+    const int stage_slots = row_slots * groups, stage = stage_slots / 8 * nb * 32;  // uint4
     const int stages = (t_end - t_begin + stage_slots - 1) / stage_slots;
     for (int s = 0; s < kRowStages - 1; ++s) {
         if (s < stages) copy_slots(a, keys, t_begin + s * stage_slots, stage_slots, t_end, ring + s * stage);
@@ -498,12 +637,12 @@ __global__ void __launch_bounds__(kScoreThreads, 2) k_score_rows(const __grid_co
                 copy_slots(a, keys, t_begin + next * stage_slots, stage_slots, t_end, ring + next % kRowStages * stage);
             asm volatile("cp.async.commit_group;\n" ::: "memory");
         }
-        const int t0 = t_begin + s * stage_slots + sg * kRowSlots;
-        const uint4 *tile = ring + s % kRowStages * stage + sg * (kRowSlots / 8) * nb * 32 + lane;
+        const int t0 = t_begin + s * stage_slots + sg * row_slots;
+        const uint4 *tile = ring + s % kRowStages * stage + sg * (row_slots / 8) * nb * 32 + lane;
         if (rw >= nr || t0 >= t_end) continue;
-        const bool whole = t0 + kRowSlots <= min(t_end, sp.begin + 1);
+        const bool whole = t0 + row_slots <= min(t_end, sp.begin + 1);
 #pragma unroll 1
-        for (int n0 = 0; n0 < kRowSlots / 8; n0 += 4) {
+        for (int n0 = 0; n0 < row_slots / 8; n0 += 4) {
             float c[4][MR][4];
 #pragma unroll
             for (int n = 0; n < 4; ++n)
@@ -697,6 +836,7 @@ __global__ void __launch_bounds__(kScoreThreads, 2) k_score_slots(const __grid_c
 
 constexpr size_t kScoreAlign = 256;
 int64_t ceil_div(int64_t x, int64_t y) { return (x + y - 1) / y; }
+size_t align_up(size_t x) { return (x + kScoreAlign - 1) / kScoreAlign * kScoreAlign; }
 
 // How a call is laid out: blocks of a cluster, rows of a row tile, slots whose
 // products fit.  Two blocks share an SM (110 KB each).
@@ -767,8 +907,79 @@ int launch_score(const ScoreArgs &a, size_t smem, int dtype_index, int nb_index,
     return SPEC_OK;
 }
 
-// Many rows: taken for bf16 from kManyMin rows a key head on.
-constexpr int kManyMin = 48;
+// Few rows: while storing the products (8 bytes each, there and back) moves
+// less than a second read of the keys.
+bool few_rows(bool f32, int R, int D) { return R <= kFewRows && 8 * R < D * (f32 ? 4 : 2); }
+
+struct FewPlan {
+    int part, chunks, pitch;
+    size_t stats_bytes, held_bytes;
+};
+// Chunks of up to 1024 slots, halved while that leaves less than four blocks
+// a SM.
+FewPlan few_plan(int B, int H, int R, int C)
+{
+    FewPlan p;
+    const int64_t heads = static_cast<int64_t>(B) * H;
+    p.part = 1024;
+    while (p.part > kPartSlots && heads * ceil_div(C, p.part) < 4 * 148) p.part /= 2;
+    p.chunks = static_cast<int>(ceil_div(C, p.part));
+    p.pitch = static_cast<int>(ceil_div(C, 32) * 32);
+    p.stats_bytes = align_up(sizeof(float2) * static_cast<size_t>(heads) * R * p.chunks);
+    p.held_bytes = align_up(sizeof(float) * static_cast<size_t>(heads) * R * p.pitch);
+    return p;
+}
+
+bool g_few_attr[64][2][3][3];
+
+template <class Tag, int NB, int NT>
+int launch_few(const ScoreArgs &a, int dtype_index, int nb_index, int nt_index, cudaStream_t st)
+{
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return SPEC_ECUDA;
+    const int nb = (a.D + 31) / 32;
+    const size_t smem = static_cast<size_t>(ceil_div(a.R, 8)) * nb * 512 * Parts<Tag>::kParts;
+    {
+        std::lock_guard<std::mutex> lock(g_score_mu);
+        if (!g_few_attr[dev][dtype_index][nb_index][nt_index]) {
+            if (cudaFuncSetAttribute(k_score_few<Tag, NB, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                     NT * NB * 512 * Parts<Tag>::kParts) != cudaSuccess)
+                return SPEC_ECUDA;
+            g_few_attr[dev][dtype_index][nb_index][nt_index] = true;
+        }
+    }
+    const unsigned heads = static_cast<unsigned>(a.B * a.H);
+    k_score_few<Tag, NB, NT><<<dim3(static_cast<unsigned>(a.chunks), heads), kScoreThreads, smem, st>>>(a);
+    if (cudaGetLastError() != cudaSuccess) return SPEC_ECUDA;
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.gridDim = dim3(static_cast<unsigned>(ceil_div(a.C, kScoreThreads)), heads);
+    cfg.blockDim = dim3(kScoreThreads);
+    cfg.stream = st;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaLaunchKernelEx(&cfg, k_score_sum, a) != cudaSuccess) {
+        (void)cudaGetLastError();
+        return SPEC_ECUDA;
+    }
+    return SPEC_OK;
+}
+template <class Tag, int NB>
+int launch_few(const ScoreArgs &a, int dtype_index, int nb_index, cudaStream_t st)
+{
+    if (a.R <= 8) return launch_few<Tag, NB, 1>(a, dtype_index, nb_index, 0, st);
+    if (a.R <= 16) return launch_few<Tag, NB, 2>(a, dtype_index, nb_index, 1, st);
+    return launch_few<Tag, NB, 4>(a, dtype_index, nb_index, 2, st);
+}
+template <class Tag>
+int launch_few(const ScoreArgs &a, int dtype_index, cudaStream_t st)
+{
+    if (a.D <= 64) return launch_few<Tag, 2>(a, dtype_index, 0, st);
+    if (a.D <= 128) return launch_few<Tag, 4>(a, dtype_index, 1, st);
+    return launch_few<Tag, 8>(a, dtype_index, 2, st);
+}
 
 // Chunks of slots of the statistics step and slots of a block of the weights
 // step: about two blocks a SM for each, in whole stages.
@@ -788,7 +999,6 @@ ManyPlan many_plan(int B, int H, int R, int C)
     p.stats_bytes = sizeof(float2) * static_cast<size_t>(heads) * R * p.chunks;
     return p;
 }
-bool many_rows(bool f32, int R) { return !f32 && R >= kManyMin; }
 
 bool g_many_attr[64][3];
 
@@ -809,12 +1019,21 @@ int launch_many(ScoreArgs a, int nb_index, cudaStream_t st)
         }
     }
     const int nb = (a.D + 31) / 32, top = std::min(a.R, kManyRows);
-    const int wr = static_cast<int>(ceil_div(top, 16 * MR)), groups = std::max(1, kScoreWarps / wr);
-    const size_t ring = static_cast<size_t>(kRowStages) * kRowSlots / 8 * groups * nb * 512;
+    // warps beyond the rows' take slots of their own, as far as their stages
+    // leave room for two blocks a SM: 64 slots each for one or two groups, 32
+    // for more
+    const int wr = static_cast<int>(ceil_div(top, 16 * MR));
+    const int fit = static_cast<int>(kScoreSmem / (kRowStages * 32 / 8 * nb * 512));
+    const int groups = std::max(1, std::min(kScoreWarps / wr, fit));
+    const int row_slots = groups > fit / 2 ? 32 : 64;
+    const size_t ring = static_cast<size_t>(kRowStages) * row_slots / 8 * groups * nb * 512;
+    const int slots = a.slots;
+    a.slots = row_slots;
     const unsigned heads = static_cast<unsigned>(a.B * a.H);
     k_score_rows<NB, MR><<<dim3(static_cast<unsigned>(a.chunks), static_cast<unsigned>(ceil_div(a.R, kManyRows)), heads),
                            32 * wr * groups, ring, st>>>(a);
     if (cudaGetLastError() != cudaSuccess) return SPEC_ECUDA;
+    a.slots = slots;
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -849,11 +1068,16 @@ extern "C" size_t spec_score_workspace_size(int batch, int queries, int q_heads,
 {
     if (batch < 0 || queries < 1 || kv_heads < 1 || q_heads < kv_heads || q_heads % kv_heads != 0 || capacity < 1)
         return 0;
-    // both types fit: the statistics of the kernels for many rows
     const int64_t rows = static_cast<int64_t>(queries) * (q_heads / kv_heads);
-    if (rows < kManyMin || rows > INT_MAX) return kScoreAlign;
-    const size_t n = many_plan(batch > 0 ? batch : 1, kv_heads, static_cast<int>(rows), capacity).stats_bytes;
-    return std::max(kScoreAlign, (n + kScoreAlign - 1) / kScoreAlign * kScoreAlign);
+    if (rows > INT_MAX) return 0;
+    const int B = std::max(batch, 1), R = static_cast<int>(rows);
+    // whichever form a type and head dimension takes
+    size_t n = kScoreAlign;
+    if (R <= kFewRows) {
+        const FewPlan p = few_plan(B, kv_heads, R, capacity);
+        n = std::max(n, p.stats_bytes + p.held_bytes);
+    }
+    return std::max(n, align_up(many_plan(B, kv_heads, R, capacity).stats_bytes));
 }
 
 extern "C" int spec_cache_score(const void *q, const void *k, spec_dtype_t dtype, int64_t q_request_stride,
@@ -888,9 +1112,7 @@ extern "C" int spec_cache_score(const void *q, const void *k, spec_dtype_t dtype
     if (!workspace || (reinterpret_cast<uintptr_t>(workspace) % kScoreAlign) != 0 || workspace_bytes < spec_score_workspace_size(batch, queries, q_heads, kv_heads, capacity))
         return SPEC_EWORKSPACE;
     const bool f32 = dtype == SPEC_F32;
-    const ScorePlan plan =
-        score_plan(batch, kv_heads, queries * (q_heads / kv_heads), head_dim, capacity, f32);
-    if (static_cast<int64_t>(batch) * kv_heads * plan.blocks > INT_MAX) return SPEC_EUNSUPPORTED;
+    if (static_cast<int64_t>(batch) * kv_heads > 65535) return SPEC_EUNSUPPORTED;
     ScoreArgs a;
     std::memset(&a, 0, sizeof a);
     a.q = q;
@@ -909,26 +1131,35 @@ extern "C" int spec_cache_score(const void *q, const void *k, spec_dtype_t dtype
     a.G = q_heads / kv_heads;
     a.D = head_dim;
     a.C = capacity;
+    a.R = a.Q * a.G;
+    a.scale2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634074);
+    a.in = scores;
+    a.out = out_scores;
+    a.status = status;
+    a.stats = static_cast<float2 *>(workspace);
+    if (few_rows(f32, a.R, head_dim)) {
+        const FewPlan few = few_plan(batch, kv_heads, a.R, capacity);
+        a.part = few.part;
+        a.chunks = few.chunks;
+        a.pitch = few.pitch;
+        a.held = reinterpret_cast<float *>(static_cast<char *>(workspace) + few.stats_bytes);
+        return f32 ? launch_few<F32>(a, 0, stream) : launch_few<Bf16>(a, 1, stream);
+    }
+    if (!f32) {
+        const ManyPlan many = many_plan(batch, kv_heads, a.R, capacity);
+        a.part = many.part;
+        a.chunks = many.chunks;
+        a.slots = many.slots;
+        if (head_dim <= 64) return launch_many<2, 2>(a, 0, stream);
+        if (head_dim <= 128) return launch_many<4, 2>(a, 1, stream);
+        return launch_many<8, 1>(a, 2, stream);
+    }
+    const ScorePlan plan = score_plan(batch, kv_heads, a.R, head_dim, capacity, f32);
+    if (static_cast<int64_t>(batch) * kv_heads * plan.blocks > INT_MAX) return SPEC_EUNSUPPORTED;
     a.blocks = plan.blocks;
     a.tile_rows = plan.tile_rows;
     a.held_rows = plan.held_rows;
     a.part = plan.part;
     a.pitch = plan.pitch;
-    a.scale2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634074);
-    a.in = scores;
-    a.out = out_scores;
-    a.status = status;
-    a.R = a.Q * a.G;
-    if (many_rows(f32, a.R)) {
-        if (static_cast<int64_t>(batch) * kv_heads > 65535) return SPEC_EUNSUPPORTED;
-        const ManyPlan many = many_plan(batch, kv_heads, a.R, capacity);
-        a.part = many.part;
-        a.chunks = many.chunks;
-        a.slots = many.slots;
-        a.stats = static_cast<float2 *>(workspace);
-        if (head_dim <= 64) return launch_many<2, 2>(a, 0, stream);
-        if (head_dim <= 128) return launch_many<4, 2>(a, 1, stream);
-        return launch_many<8, 1>(a, 2, stream);
-    }
-    return f32 ? launch_score<F32>(a, plan.smem, 0, stream) : launch_score<Bf16>(a, plan.smem, 1, stream);
+    return launch_score<F32>(a, plan.smem, 0, stream);
 }

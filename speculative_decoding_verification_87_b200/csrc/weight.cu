@@ -31,6 +31,7 @@
 #include <cstdint>
 #include <cstring>
 #include <mutex>
+#include <type_traits>
 
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
@@ -102,6 +103,23 @@ __device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1
                  "{%0,%1,%2,%3};\n"
                  : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
                  : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// The same with a zero accumulator.
+__device__ __forceinline__ void mma_bf16_first(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                               uint32_t b0, uint32_t b1)
+{
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+                 "{%10,%10,%10,%10};\n"
+                 : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
+
+__device__ __forceinline__ unsigned long long f2_ex2(unsigned long long x)
+{
+    float lo, hi;
+    f2_unpack(x, lo, hi);
+    return f2_pack(ex2_approx(lo), ex2_approx(hi));
 }
 
 // Eight elements of a vector as bf16 pairs: themselves, or the three parts
@@ -193,11 +211,10 @@ struct Slots {
 
 // Rows [r0, r0 + 8 * tiles) of head h below `rows`, as B fragments: 512
 // bytes per (n-tile, 32 elements, part), a lane's 16 bytes in place.
-template <class Tag, int NB>
-__device__ __forceinline__ void stage_rows(const ScoreArgs &a, int b, int h, int r0, int rows, int tiles, uint4 *sq)
+template <class Tag>
+__device__ __forceinline__ void stage_rows(const ScoreArgs &a, int b, int h, int r0, int rows, int tiles, int nb, uint4 *sq)
 {
     constexpr int kP = Parts<Tag>::kParts;
-    const int nb = (a.D + 31) / 32;
     for (int i = threadIdx.x; i < tiles * nb * 32; i += kScoreThreads) {
         const int lane = i & 31, j = (i >> 5) % nb, tile = (i >> 5) / nb;
         const int r = r0 + tile * 8 + (lane >> 2);
@@ -288,7 +305,7 @@ __global__ void __launch_bounds__(kScoreThreads, 2) k_score(const __grid_constan
         // a row's slots are shared by `split` warps where rows are few
         const int split = nr <= 1 ? 8 : nr <= 2 ? 4 : nr <= 4 ? 2 : 1;
         __syncthreads();
-        stage_rows<Tag, NB>(a, b, h, r0, rows, tiles, sq);
+        stage_rows<Tag>(a, b, h, r0, rows, tiles, nb, sq);
         for (int i = tid; i < nr * split; i += kScoreThreads) stat[i] = make_float2(-INFINITY, 0.f);
         __syncthreads();
 
@@ -437,7 +454,7 @@ __global__ void __launch_bounds__(kScoreThreads, 2) k_score_few(const __grid_con
     Slots<Tag, NB> cur, next;
     int t0 = t_begin + warp * 16;
     if (t0 < t_end) cur.load(a, keys, t0, t_end);
-    stage_rows<Tag, NB>(a, b, h, 0, rows, tiles, sq);
+    stage_rows<Tag>(a, b, h, 0, rows, tiles, nb, sq);
     __syncthreads();
     float m[NT][2], l[NT][2];
 #pragma unroll
@@ -562,16 +579,18 @@ constexpr int kManyRows = 128;     // rows of a row tile
 constexpr int kRowStages = 3;
 
 // Slots [t0, t0 + slots) below `end` as B fragments (512 bytes per 8 slots
-// and 32 elements), asynchronously; the rest as zeros.
+// and 32 elements, NB * 32 elements a slot), asynchronously; the rest as
+// zeros.
+template <int NB>
 __device__ __forceinline__ void copy_slots(const ScoreArgs &a, const uint16_t *keys, int t0, int slots, int end, uint4 *dst)
 {
-    const int nb = (a.D + 31) / 32, chunks = nb * 4;
-    for (int i = threadIdx.x; i < slots * chunks; i += blockDim.x) {
-        const int slot = i / chunks, c = i - slot * chunks;
+    constexpr int kChunks = 4 * NB;
+    for (int i = threadIdx.x; i < slots * kChunks; i += blockDim.x) {
+        const int slot = i / kChunks, c = i % kChunks;
         const bool in = t0 + slot < end && c * 8 < a.D;
         const uint16_t *from = in ? keys + (t0 + slot) * a.k_slot + c * 8 : keys;
         const uint32_t at = static_cast<uint32_t>(
-            __cvta_generic_to_shared(dst + ((slot >> 3) * nb + (c >> 2)) * 32 + (slot & 7) * 4 + (c & 3)));
+            __cvta_generic_to_shared(dst + ((slot >> 3) * NB + (c >> 2)) * 32 + (slot & 7) * 4 + (c & 3)));
         asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(at), "l"(from), "r"(in ? 16 : 0) : "memory");
     }
 }
@@ -591,17 +610,17 @@ __global__ void __launch_bounds__(kScoreThreads, 2) k_score_rows(const __grid_co
     const int t_begin = blockIdx.x * a.part, t_end = min(sp.end, t_begin + a.part);
     asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
     if (!sp.ok || r0 >= rows || t_begin >= t_end) return;
-    const int nr = min(rows - r0, kManyRows), nb = (a.D + 31) / 32;
+    const int nr = min(rows - r0, kManyRows);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
     const int wr = (min(a.R, kManyRows) + 16 * MR - 1) / (16 * MR);  // warps over the rows
     const int groups = (blockDim.x >> 5) / wr;                          // groups of them over the slots
     const int row_slots = a.slots;                                      // of a stage, for each group
     const int rw = (warp % wr) * 16 * MR, sg = warp / wr;
     const auto *keys = static_cast<const uint16_t *>(a.k) + b * a.k_req + h * a.k_head;
-    const int stage_slots = row_slots * groups, stage = stage_slots / 8 * nb * 32;  // uint4
+    const int stage_slots = row_slots * groups, stage = stage_slots / 8 * NB * 32;  // uint4
     const int stages = (t_end - t_begin + stage_slots - 1) / stage_slots;
     for (int s = 0; s < kRowStages - 1; ++s) {
-        if (s < stages) copy_slots(a, keys, t_begin + s * stage_slots, stage_slots, t_end, ring + s * stage);
+        if (s < stages) copy_slots<NB>(a, keys, t_begin + s * stage_slots, stage_slots, t_end, ring + s * stage);
         asm volatile("cp.async.commit_group;\n" ::: "memory");
     }
     // this warp's rows: lane (g, t) holds rows g and g + 8 of each 16
@@ -628,71 +647,74 @@ __global__ void __launch_bounds__(kScoreThreads, 2) k_score_rows(const __grid_co
     for (int i = 0; i < MR; ++i) m[i][0] = m[i][1] = -INFINITY, l[i][0] = l[i][1] = 0.f;
     const float sc = a.scale2;
 
+    // 32 slots from t0 on, as fragments at `tile`; `whole`: seen by every row
+    auto step = [&](const uint4 *tile, int t0, auto whole) {
+        float c[4][MR][4];
+#pragma unroll
+        for (int j = 0; j < NB; ++j)
+#pragma unroll
+            for (int n = 0; n < 4; ++n) {
+                const uint4 w = tile[(n * NB + j) * 32];
+#pragma unroll
+                for (int i = 0; i < MR; ++i) {
+                    const uint4 u = q[i][j][0], v = q[i][j][1];
+                    if (j == 0) mma_bf16_first(c[n][i], u.x, v.x, u.y, v.y, w.x, w.y);
+                    else mma_bf16(c[n][i], u.x, v.x, u.y, v.y, w.x, w.y);
+                    mma_bf16(c[n][i], u.z, v.z, u.w, v.w, w.z, w.w);
+                }
+            }
+#pragma unroll
+        for (int i = 0; i < MR; ++i)
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                // the scaled products are rounded here and in k_score_slots
+                // alike: fused, they would differ from L's by half a step of s
+                float x[8];
+#pragma unroll
+                for (int n = 0; n < 4; ++n)
+                    x[2 * n] = __fmul_rn(c[n][i][2 * half], sc), x[2 * n + 1] = __fmul_rn(c[n][i][2 * half + 1], sc);
+                if (!whole) {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        const int slot = t0 + (e >> 1) * 8 + 2 * t + (e & 1);
+                        if (!(slot < t_end && slot <= last[i][half])) x[e] = -INFINITY;
+                    }
+                }
+                float top = x[0];
+#pragma unroll
+                for (int e = 1; e < 8; ++e) top = fmaxf(top, x[e]);
+                if (top > m[i][half]) {
+                    l[i][half] *= ex2_approx(m[i][half] - top);
+                    m[i][half] = top;
+                }
+                const float mm = !whole && m[i][half] == -INFINITY ? 0.f : m[i][half];
+                const unsigned long long nm = f2_pack(-mm, -mm);
+                unsigned long long e01 = f2_ex2(f2_add(f2_pack(x[0], x[1]), nm));
+#pragma unroll
+                for (int n = 1; n < 4; ++n) e01 = f2_add(e01, f2_ex2(f2_add(f2_pack(x[2 * n], x[2 * n + 1]), nm)));
+                float e0, e1;
+                f2_unpack(e01, e0, e1);
+                l[i][half] += e0 + e1;
+            }
+    };
     for (int s = 0; s < stages; ++s) {
         asm volatile("cp.async.wait_group %0;\n" ::"n"(kRowStages - 2) : "memory");
         __syncthreads();
         {
             const int next = s + kRowStages - 1;
             if (next < stages)
-                copy_slots(a, keys, t_begin + next * stage_slots, stage_slots, t_end, ring + next % kRowStages * stage);
+                copy_slots<NB>(a, keys, t_begin + next * stage_slots, stage_slots, t_end, ring + next % kRowStages * stage);
             asm volatile("cp.async.commit_group;\n" ::: "memory");
         }
         const int t0 = t_begin + s * stage_slots + sg * row_slots;
-        const uint4 *tile = ring + s % kRowStages * stage + sg * (row_slots / 8) * nb * 32 + lane;
+        const uint4 *tile = ring + s % kRowStages * stage + sg * (row_slots / 8) * NB * 32 + lane;
         if (rw >= nr || t0 >= t_end) continue;
-        const bool whole = t0 + row_slots <= min(t_end, sp.begin + 1);
+        if (t0 + row_slots <= min(t_end, sp.begin + 1)) {
 #pragma unroll 1
-        for (int n0 = 0; n0 < row_slots / 8; n0 += 4) {
-            float c[4][MR][4];
-#pragma unroll
-            for (int n = 0; n < 4; ++n)
-#pragma unroll
-                for (int i = 0; i < MR; ++i) c[n][i][0] = c[n][i][1] = c[n][i][2] = c[n][i][3] = 0.f;
-#pragma unroll
-            for (int j = 0; j < NB; ++j)
-                if (j < nb) {
-#pragma unroll
-                    for (int n = 0; n < 4; ++n) {
-                        const uint4 w = tile[((n0 + n) * nb + j) * 32];
-#pragma unroll
-                        for (int i = 0; i < MR; ++i) {
-                            const uint4 u = q[i][j][0], v = q[i][j][1];
-                            mma_bf16(c[n][i], u.x, v.x, u.y, v.y, w.x, w.y);
-                            mma_bf16(c[n][i], u.z, v.z, u.w, v.w, w.z, w.w);
-                        }
-                    }
-                }
-#pragma unroll
-            for (int i = 0; i < MR; ++i)
-#pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                    float x[8];
-#pragma unroll
-                    for (int n = 0; n < 4; ++n)
-#pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            // rounded, here and in k_score_slots alike: a fused
-                            // product would differ from L's by half a step of s
-                            x[2 * n + e] = __fmul_rn(c[n][i][2 * half + e], sc);
-                            const int slot = t0 + (n0 + n) * 8 + 2 * t + e;
-                            if (!whole && !(slot < t_end && slot <= last[i][half])) x[2 * n + e] = -INFINITY;
-                        }
-                    float top = x[0];
-#pragma unroll
-                    for (int e = 1; e < 8; ++e) top = fmaxf(top, x[e]);
-                    if (top > m[i][half]) {
-                        l[i][half] *= ex2_approx(m[i][half] - top);
-                        m[i][half] = top;
-                    }
-                    const float mm = m[i][half] == -INFINITY ? 0.f : m[i][half];
-                    float e0 = 0.f, e1 = 0.f;
-#pragma unroll
-                    for (int e = 0; e < 8; e += 2) {
-                        e0 += ex2_approx(x[e] - mm);
-                        e1 += ex2_approx(x[e + 1] - mm);
-                    }
-                    l[i][half] += e0 + e1;
-                }
+            for (int n0 = 0; n0 < row_slots; n0 += 32) step(tile + n0 / 8 * NB * 32, t0 + n0, std::true_type{});
+        } else {
+#pragma unroll 1
+            for (int n0 = 0; n0 < row_slots; n0 += 32) step(tile + n0 / 8 * NB * 32, t0 + n0, std::false_type{});
         }
     }
     asm volatile("cp.async.wait_group 0;\n" ::: "memory");
@@ -728,7 +750,7 @@ __global__ void __launch_bounds__(kScoreThreads, 2) k_score_slots(const __grid_c
     constexpr int kM = NB <= 4 ? 2 : 1;  // m-tiles of 16 slots a warp
     extern __shared__ __align__(16) unsigned char smem[];
     uint4 *sq = reinterpret_cast<uint4 *>(smem);
-    __shared__ float L[kManyRows];
+    __shared__ __align__(8) float minus_l[kManyRows];
     const int64_t head = blockIdx.y;
     const int b = static_cast<int>(head / a.H), h = static_cast<int>(head % a.H);
     const Span sp = span_of(a, b);
@@ -739,7 +761,7 @@ __global__ void __launch_bounds__(kScoreThreads, 2) k_score_slots(const __grid_c
     const int rows = (sp.end - sp.begin) * a.G;
     const int t_begin = blockIdx.x * a.slots, t_end = min(sp.end, t_begin + a.slots);
     if (t_begin >= t_end) return;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3, nb = (a.D + 31) / 32;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
     const auto *keys = static_cast<const uint16_t *>(a.k) + b * a.k_req + h * a.k_head;
     const float *in = a.in + head * a.C;
     float *out = a.out + head * a.C;
@@ -748,7 +770,7 @@ __global__ void __launch_bounds__(kScoreThreads, 2) k_score_slots(const __grid_c
     for (int r0 = 0; r0 < max(rows, 1); r0 += kManyRows) {
         const int nr = min(rows - r0, kManyRows), tiles = (nr + 7) / 8;
         __syncthreads();
-        stage_rows<Bf16, NB>(a, b, h, r0, rows, tiles, sq);
+        stage_rows<Bf16>(a, b, h, r0, rows, tiles, NB, sq);
         if (r0 == 0) asm volatile("griddepcontrol.wait;\n" ::: "memory");
         // eight lanes a row merge the chunks' statistics
         for (int i = threadIdx.x; i < tiles * 64; i += kScoreThreads) {
@@ -767,13 +789,14 @@ __global__ void __launch_bounds__(kScoreThreads, 2) k_score_slots(const __grid_c
                 if (ol != ol) ll = ol;
             }
             // a row that is none weighs nothing
-            if ((i & 7) == 0) L[r] = r < nr ? mm + log2f(ll) : INFINITY;
+            if ((i & 7) == 0) minus_l[r] = r < nr ? -(mm + log2f(ll)) : -INFINITY;
         }
         __syncthreads();
         for (int t0 = t_begin + warp * 16 * kM; t0 < t_end; t0 += kScoreWarps * 16 * kM) {
             uint4 k[kM][NB][2];
-            float old[kM][2], sum[kM][2];
-            int first[kM][2];  // the first row that sees the slot
+            float old[kM][2];
+            unsigned long long sum[kM][2];  // of this lane's even and odd rows
+            int first[kM][2];               // the first row that sees the slot
 #pragma unroll
             for (int i = 0; i < kM; ++i)
 #pragma unroll
@@ -787,44 +810,53 @@ __global__ void __launch_bounds__(kScoreThreads, 2) k_score_slots(const __grid_c
                         k[i][j][half] = raw[0];
                     }
                     old[i][half] = t != 0 || slot >= t_end ? 0.f : r0 > 0 ? out[slot] : slot < sp.begin ? in[slot] : 0.f;
-                    sum[i][half] = 0.f;
+                    sum[i][half] = f2_pack(0.f, 0.f);
                     first[i][half] = max(0, (slot - sp.begin) * a.G - r0);
                 }
-            const bool whole = t0 + 16 * kM <= sp.begin + 1;
-#pragma unroll 2
-            for (int n = 0; n < tiles; ++n) {
+            // rows 8 n .. 8 n + 7; `whole`: the slots are seen by every row
+            auto step = [&](int n, auto whole) {
                 float c[kM][4];
 #pragma unroll
-                for (int i = 0; i < kM; ++i) c[i][0] = c[i][1] = c[i][2] = c[i][3] = 0.f;
+                for (int j = 0; j < NB; ++j) {
+                    const uint4 w = sq[(n * NB + j) * 32 + lane];
 #pragma unroll
-                for (int j = 0; j < NB; ++j)
-                    if (j < nb) {
-                        const uint4 w = sq[(n * nb + j) * 32 + lane];
-#pragma unroll
-                        for (int i = 0; i < kM; ++i) {
-                            const uint4 u = k[i][j][0], v = k[i][j][1];
-                            mma_bf16(c[i], u.x, v.x, u.y, v.y, w.x, w.y);
-                            mma_bf16(c[i], u.z, v.z, u.w, v.w, w.z, w.w);
-                        }
+                    for (int i = 0; i < kM; ++i) {
+                        const uint4 u = k[i][j][0], v = k[i][j][1];
+                        if (j == 0) mma_bf16_first(c[i], u.x, v.x, u.y, v.y, w.x, w.y);
+                        else mma_bf16(c[i], u.x, v.x, u.y, v.y, w.x, w.y);
+                        mma_bf16(c[i], u.z, v.z, u.w, v.w, w.z, w.w);
                     }
-                const float2 y = *reinterpret_cast<const float2 *>(&L[n * 8 + 2 * t]);
+                }
+                const unsigned long long y = *reinterpret_cast<const unsigned long long *>(&minus_l[n * 8 + 2 * t]);
 #pragma unroll
                 for (int i = 0; i < kM; ++i)
 #pragma unroll
                     for (int half = 0; half < 2; ++half) {
-                        float z0 = __fmul_rn(c[i][2 * half], sc) - y.x, z1 = __fmul_rn(c[i][2 * half + 1], sc) - y.y;
+                        unsigned long long z = f2_add(f2_pack(__fmul_rn(c[i][2 * half], sc), __fmul_rn(c[i][2 * half + 1], sc)), y);
                         if (!whole) {
+                            float z0, z1;
+                            f2_unpack(z, z0, z1);
                             if (n * 8 + 2 * t < first[i][half]) z0 = -INFINITY;
                             if (n * 8 + 2 * t + 1 < first[i][half]) z1 = -INFINITY;
+                            z = f2_pack(z0, z1);
                         }
-                        sum[i][half] += ex2_approx(z0) + ex2_approx(z1);
+                        sum[i][half] = f2_add(sum[i][half], f2_ex2(z));
                     }
+            };
+            if (t0 + 16 * kM <= sp.begin + 1) {
+#pragma unroll 2
+                for (int n = 0; n < tiles; ++n) step(n, std::true_type{});
+            } else {
+#pragma unroll 1
+                for (int n = 0; n < tiles; ++n) step(n, std::false_type{});
             }
 #pragma unroll
             for (int i = 0; i < kM; ++i)
 #pragma unroll
                 for (int half = 0; half < 2; ++half) {
-                    float x = sum[i][half];
+                    float x, x1;
+                    f2_unpack(sum[i][half], x, x1);
+                    x += x1;
                     x += __shfl_xor_sync(kFull, x, 1);
                     x += __shfl_xor_sync(kFull, x, 2);
                     const int slot = t0 + 16 * i + g + 8 * half;
@@ -1018,15 +1050,15 @@ int launch_many(ScoreArgs a, int nb_index, cudaStream_t st)
             g_many_attr[dev][nb_index] = true;
         }
     }
-    const int nb = (a.D + 31) / 32, top = std::min(a.R, kManyRows);
+    const int top = std::min(a.R, kManyRows);
     // warps beyond the rows' take slots of their own, as far as their stages
     // leave room for two blocks a SM: 64 slots each for one or two groups, 32
     // for more
     const int wr = static_cast<int>(ceil_div(top, 16 * MR));
-    const int fit = static_cast<int>(kScoreSmem / (kRowStages * 32 / 8 * nb * 512));
+    const int fit = static_cast<int>(kScoreSmem / (kRowStages * 32 / 8 * NB * 512));
     const int groups = std::max(1, std::min(kScoreWarps / wr, fit));
     const int row_slots = groups > fit / 2 ? 32 : 64;
-    const size_t ring = static_cast<size_t>(kRowStages) * row_slots / 8 * groups * nb * 512;
+    const size_t ring = static_cast<size_t>(kRowStages) * row_slots / 8 * groups * NB * 512;
     const int slots = a.slots;
     a.slots = row_slots;
     const unsigned heads = static_cast<unsigned>(a.B * a.H);
@@ -1040,7 +1072,7 @@ int launch_many(ScoreArgs a, int nb_index, cudaStream_t st)
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.gridDim = dim3(static_cast<unsigned>(ceil_div(a.C, a.slots)), heads);
     cfg.blockDim = dim3(kScoreThreads);
-    cfg.dynamicSmemBytes = ceil_div(top, 8) * nb * 512;
+    cfg.dynamicSmemBytes = ceil_div(top, 8) * NB * 512;
     cfg.stream = st;
     cfg.attrs = attr;
     cfg.numAttrs = 1;

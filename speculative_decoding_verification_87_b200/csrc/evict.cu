@@ -23,7 +23,7 @@ namespace {
 
 namespace cg = cooperative_groups;
 
-constexpr int kPickThreads = 1024;
+constexpr int kPickThreads = 512;  // two blocks a SM: with 1024 threads only some 14 clusters of 8 fit the GPU at once
 constexpr int kPickWarps = kPickThreads / 32;
 constexpr int kClusterMax = 8;
 constexpr int kSliceMax = SPEC_MAX_SLOTS / kClusterMax;  // keys of a block: 128 KB at most
@@ -77,7 +77,7 @@ struct alignas(16) Shown {
     int counts[2][2];  // of this block's slice, for cluster-wide prefixes
 };
 
-__global__ void __launch_bounds__(kPickThreads, 1) k_evict_pick(const __grid_constant__ EvictArgs a)
+__global__ void __launch_bounds__(kPickThreads, 2) k_evict_pick(const __grid_constant__ EvictArgs a)
 {
     extern __shared__ uint32_t keys[];
     __shared__ Shown sh;
@@ -122,7 +122,7 @@ __global__ void __launch_bounds__(kPickThreads, 1) k_evict_pick(const __grid_con
     for (int i = tid; i < 3 * kBins; i += kPickThreads) (&sh.hist[0][0])[i] = 0;
     __syncthreads();
     if (warp == 0) {
-        newest = __reduce_max_sync(kAll, warp_sum[0][lane]);
+        newest = __reduce_max_sync(kAll, warp_sum[0][lane % kPickWarps]);
         if (lane == 0) sh.newest = newest;
     }
     cluster.sync();
@@ -153,31 +153,36 @@ __global__ void __launch_bounds__(kPickThreads, 1) k_evict_pick(const __grid_con
             if ((key & mask) == prefix) atomicAdd(&sh.hist[pass][(key >> shift) & digit], 1);
         }
         cluster.sync();
-        // two bins a thread from the top, hi and hi - 1, over all blocks
-        const int hi = kBins - 1 - 2 * tid;
-        int c0 = 0, c1 = 0;
+        // four bins a thread from the top, hi .. hi - 3, over all blocks
+        static_assert(kBins == 4 * kPickThreads, "four bins a thread");
+        const int hi = kBins - 1 - 4 * tid;
+        int c[4] = {0, 0, 0, 0};
 #pragma unroll
         for (int r = 0; r < kClusterMax; ++r)
             if (r < blocks) {
-                const int2 x = *reinterpret_cast<const int2 *>(&cluster.map_shared_rank(&sh, r)->hist[pass][hi - 1]);
-                c0 += x.y;
-                c1 += x.x;
+                const int4 x = *reinterpret_cast<const int4 *>(&cluster.map_shared_rank(&sh, r)->hist[pass][hi - 3]);
+                c[0] += x.w;
+                c[1] += x.z;
+                c[2] += x.y;
+                c[3] += x.x;
             }
-        const int incl = warp_inclusive(c0 + c1);
+        const int sum = c[0] + c[1] + c[2] + c[3], incl = warp_inclusive(sum);
         if (lane == 31) warp_sum[0][warp] = incl;
         __syncthreads();
         if (warp == 0) {
-            const int w = warp_sum[0][lane];
-            warp_sum[1][lane] = warp_inclusive(w) - w;
+            const int w = lane < kPickWarps ? warp_sum[0][lane] : 0;
+            const int before = warp_inclusive(w) - w;
+            if (lane < kPickWarps) warp_sum[1][lane] = before;
         }
         __syncthreads();
-        const int above = incl - (c0 + c1) + warp_sum[1][warp];
-        if (above < want && above + c0 >= want) {
-            pick_bin = hi;
-            pick_above = above;
-        } else if (above + c0 < want && above + c0 + c1 >= want) {
-            pick_bin = hi - 1;
-            pick_above = above + c0;
+        int above = incl - sum + warp_sum[1][warp];
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+            if (above < want && above + c[x] >= want) {
+                pick_bin = hi - x;
+                pick_above = above;
+            }
+            above += c[x];
         }
         __syncthreads();
         prefix |= static_cast<uint32_t>(pick_bin) << shift;
@@ -199,10 +204,10 @@ __global__ void __launch_bounds__(kPickThreads, 1) k_evict_pick(const __grid_con
         }
         __syncthreads();
         if (warp < 2) {
-            const int w = warp_sum[warp][lane];
+            const int w = lane < kPickWarps ? warp_sum[warp][lane] : 0;
             const int incl = warp_inclusive(w);
             __syncwarp();
-            warp_sum[warp][lane] = incl - w;
+            if (lane < kPickWarps) warp_sum[warp][lane] = incl - w;
             if (lane == 31) sh.counts[call][warp] = incl;
         }
         cluster.sync();

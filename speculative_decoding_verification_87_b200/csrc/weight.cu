@@ -16,10 +16,12 @@
 // exponential per product.  A slice whose products do not fit is swept in
 // parts twice, once for the statistics and once for the weights.
 //
-// Products run on mma.sync m16n8k16 with the slots as rows of A, read
-// straight from global memory into fragments: the sum over d may run in any
-// order, so a lane's 16 contiguous bytes (8 elements) of a key serve as its
-// two k-steps' elements, with the queries laid out the same way.  fp32
+// Products run on mma.sync m16n8k16 with 16 rows as A and 8 slots as B.  The
+// sum over d may run in any order, so a lane's 16 contiguous bytes (8
+// elements) of a key serve as its two k-steps' elements, straight from global
+// memory as B fragments (two registers that follow one another); the queries
+// are laid out in shared memory so that one 16-byte load is an A fragment.
+// (With the slots as A every product needed four register moves.)  fp32
 // inputs are split into three bf16 parts (24 bits in all) and the six
 // products above 2^-24 are added up.
 //
@@ -47,7 +49,6 @@ namespace cg = cooperative_groups;
 
 constexpr int kScoreThreads = 256;
 constexpr int kScoreWarps = kScoreThreads / 32;
-constexpr int kGroup = 4;           // n-tiles (8 rows each) per register group
 constexpr int kClusterMax = 16;
 constexpr int kPartSlots = 128;     // a swept part is a multiple of this: 16 slots a warp
 
@@ -57,7 +58,7 @@ struct ScoreArgs {
     const int32_t *begin, *end;
     int B, Q, H, G, D, C;  // H key heads, C capacity
     int blocks;            // of a cluster
-    int tile_rows;         // rows of a row tile (a multiple of 8)
+    int tile_rows;         // rows of a row tile (a multiple of 16)
     int held_rows;         // of them, rows whose products are stored
     int part;              // slots whose products fit shared memory
     int pitch;             // words between rows of products
@@ -70,6 +71,7 @@ struct ScoreArgs {
     int chunks;            // chunks of `part` slots (statistics)
     int slots;             // slots of a block (weights), of a warp's stage (statistics)
     float2 *stats;         // [B][H][R][chunks]
+    float *minus_l;        // many rows: -L [B][H][R]
     float *held;           // few rows: products [B][H][R][pitch]
 };
 
@@ -209,57 +211,84 @@ struct Slots {
     }
 };
 
-// Rows [r0, r0 + 8 * tiles) of head h below `rows`, as B fragments: 512
-// bytes per (n-tile, 32 elements, part), a lane's 16 bytes in place.
+// Rows [r0, r0 + 16 * tiles) of head h below `rows` (the rest as zeros) as A
+// fragments: 1024 bytes per (16 rows, 32 elements, part), 512 a k-step, a
+// lane's 16 bytes in place.
 template <class Tag>
 __device__ __forceinline__ void stage_rows(const ScoreArgs &a, int b, int h, int r0, int rows, int tiles, int nb, uint4 *sq)
 {
     constexpr int kP = Parts<Tag>::kParts;
-    for (int i = threadIdx.x; i < tiles * nb * 32; i += kScoreThreads) {
-        const int lane = i & 31, j = (i >> 5) % nb, tile = (i >> 5) / nb;
-        const int r = r0 + tile * 8 + (lane >> 2);
-        uint4 raw[Parts<Tag>::kRaw], p[kP];
-        const int q = r / a.G, g = r - q * a.G;
-        const auto *row = static_cast<const typename Tag::elem *>(a.q) + b * a.q_req + q * a.q_tok +
-                          (static_cast<int64_t>(h) * a.G + g) * a.q_head;
-        load8<Tag>(row, r < rows ? 32 * j + 8 * (lane & 3) : a.D, a.D, raw);
-        Parts<Tag>::split(raw, p);
+    constexpr int kBatch = 2;  // four loads in flight a thread
+    const int threads = blockDim.x;
+    for (int i0 = threadIdx.x; i0 < tiles * nb * 32; i0 += kBatch * threads) {
+        uint4 raw[kBatch][2][Parts<Tag>::kRaw];
 #pragma unroll
-        for (int x = 0; x < kP; ++x) sq[((tile * nb + j) * kP + x) * 32 + lane] = p[x];
+        for (int x = 0; x < kBatch; ++x) {
+            const int i = i0 + x * threads, lane = i & 31, j = (i >> 5) % nb, tile = (i >> 5) / nb;
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                const int r = r0 + tile * 16 + (lane >> 2) + 8 * half, q = r / a.G, g = r - q * a.G;
+                const auto *row = static_cast<const typename Tag::elem *>(a.q) + b * a.q_req + q * a.q_tok +
+                                  (static_cast<int64_t>(h) * a.G + g) * a.q_head;
+                load8<Tag>(row, tile < tiles && r < rows ? 32 * j + 8 * (lane & 3) : a.D, a.D, raw[x][half]);
+            }
+        }
+#pragma unroll
+        for (int x = 0; x < kBatch; ++x) {
+            const int i = i0 + x * threads;
+            uint4 u[kP], v[kP];
+            Parts<Tag>::split(raw[x][0], u);
+            Parts<Tag>::split(raw[x][1], v);
+            if (i < tiles * nb * 32)
+#pragma unroll
+                for (int y = 0; y < kP; ++y) {
+                    uint4 *to = sq + ((i >> 5) * kP + y) * 64 + (i & 31);
+                    to[0] = make_uint4(u[y].x, v[y].x, u[y].y, v[y].y);
+                    to[32] = make_uint4(u[y].z, v[y].z, u[y].w, v[y].w);
+                }
+        }
     }
 }
 
-// The products of a warp's 16 slots with n-tiles [tile0, tile0 + kGroup):
-// fp32 accumulators, c[n][0..1] slot g rows 2t, 2t+1; c[n][2..3] slot g + 8.
-template <class Tag, int NB, int kGroup>
+// The products of a warp's 16 slots with the 16-row tiles [tile0, tile0 + MT):
+// c[i][half] holds slots 8 half + 2 t, + 1 of rows g ([0], [1]) and g + 8.
+template <class Tag, int NB, int MT>
 __device__ __forceinline__ void products(const Slots<Tag, NB> &k, const uint4 *sq, int nb, int tile0, int tiles,
-                                         float (&c)[kGroup][4])
+                                         float (&c)[MT][2][4])
 {
     constexpr int kP = Parts<Tag>::kParts;
     const int lane = threadIdx.x & 31;
 #pragma unroll
-    for (int n = 0; n < kGroup; ++n) c[n][0] = c[n][1] = c[n][2] = c[n][3] = 0.f;
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int half = 0; half < 2; ++half) c[i][half][0] = c[i][half][1] = c[i][half][2] = c[i][half][3] = 0.f;
 #pragma unroll
     for (int j = 0; j < NB; ++j) {
         if (j < nb) {
-            uint4 lo[kP], hi[kP];
-            k.part(j, 0, lo);
-            k.part(j, 1, hi);
+            uint4 y[2][kP];
+            k.part(j, 0, y[0]);
+            k.part(j, 1, y[1]);
 #pragma unroll
-            for (int n = 0; n < kGroup; ++n) {
-                if (tile0 + n < tiles) {
-                    uint4 y[kP];
+            for (int i = 0; i < MT; ++i) {
+                if (tile0 + i < tiles) {
+                    uint4 lo[kP], hi[kP];
 #pragma unroll
-                    for (int x = 0; x < kP; ++x) y[x] = sq[(((tile0 + n) * nb + j) * kP + x) * 32 + lane];
+                    for (int x = 0; x < kP; ++x) {
+                        const uint4 *at = sq + (((tile0 + i) * nb + j) * kP + x) * 64 + lane;
+                        lo[x] = at[0];
+                        hi[x] = at[32];
+                    }
                     // the smaller products first
 #pragma unroll
                     for (int s = kP - 1; s >= 0; --s)
 #pragma unroll
-                        for (int x = s; x >= 0; --x) {
-                            const uint4 u = lo[x], v = hi[x], w = y[s - x];
-                            mma_bf16(c[n], u.x, v.x, u.y, v.y, w.x, w.y);
-                            mma_bf16(c[n], u.z, v.z, u.w, v.w, w.z, w.w);
-                        }
+                        for (int x = s; x >= 0; --x)
+#pragma unroll
+                            for (int half = 0; half < 2; ++half) {
+                                const uint4 w = y[half][s - x];
+                                mma_bf16(c[i][half], lo[x].x, lo[x].y, lo[x].z, lo[x].w, w.x, w.y);
+                                mma_bf16(c[i][half], hi[x].x, hi[x].y, hi[x].z, hi[x].w, w.z, w.w);
+                            }
                 }
             }
         }
@@ -283,7 +312,7 @@ __global__ void __launch_bounds__(kScoreThreads, 2) k_score(const __grid_constan
     const int nb = (a.D + 31) / 32;
     // shared memory: query fragments, products, row statistics and factors
     uint4 *sq = reinterpret_cast<uint4 *>(smem);
-    float *ss = reinterpret_cast<float *>(sq + a.tile_rows / 8 * nb * Parts<Tag>::kParts * 32);
+    float *ss = reinterpret_cast<float *>(sq + a.tile_rows / 16 * nb * Parts<Tag>::kParts * 64);
     float2 *stat = reinterpret_cast<float2 *>(ss + a.held_rows * a.pitch);  // [units]
     float *fac = reinterpret_cast<float *>(stat + max(a.tile_rows, kScoreWarps));               // [units]
 
@@ -301,7 +330,7 @@ __global__ void __launch_bounds__(kScoreThreads, 2) k_score(const __grid_constan
         return;
     }
     for (int r0 = 0; r0 < rows; r0 += a.tile_rows) {
-        const int nr = min(rows - r0, a.tile_rows), tiles = (nr + 7) / 8;
+        const int nr = min(rows - r0, a.tile_rows), tiles = (nr + 15) / 16;
         // a row's slots are shared by `split` warps where rows are few
         const int split = nr <= 1 ? 8 : nr <= 2 ? 4 : nr <= 4 ? 2 : 1;
         __syncthreads();
@@ -317,20 +346,19 @@ __global__ void __launch_bounds__(kScoreThreads, 2) k_score(const __grid_constan
             for (; t0 < p1; t0 += kScoreWarps * 16) {
                 if (t0 + kScoreWarps * 16 < p1) next.load(a, keys, t0 + kScoreWarps * 16, p1);
                 const int g = lane >> 2, t2 = 2 * (lane & 3);
-                for (int tile0 = 0; tile0 < tiles; tile0 += kGroup) {
-                    float c[kGroup][4];
-                    products<Tag, NB, kGroup>(cur, sq, nb, tile0, tiles, c);
+                for (int tile0 = 0; tile0 < tiles; ++tile0) {
+                    float c[1][2][4];
+                    products<Tag, NB, 1>(cur, sq, nb, tile0, tiles, c);
 #pragma unroll
-                    for (int n = 0; n < kGroup; ++n) {
+                    for (int half = 0; half < 2; ++half)
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
-                            const int r = (tile0 + n) * 8 + t2 + (e & 1), t = t0 + g + 8 * (e >> 1);
+                            const int r = tile0 * 16 + g + 8 * (e >> 1), t = t0 + 8 * half + t2 + (e & 1);
                             if (r < nr) {
                                 const bool seen = t < p1 && (t <= sp.begin || t <= sp.begin + (r0 + r) / a.G);
-                                ss[r * a.pitch + t - p0] = seen ? c[n][e] * a.scale2 : -INFINITY;
+                                ss[r * a.pitch + t - p0] = seen ? c[0][half][e] * a.scale2 : -INFINITY;
                             }
                         }
-                    }
                 }
                 cur = next;
             }
@@ -433,13 +461,13 @@ constexpr int kFewRows = 32;
 
 // Products and statistics of one chunk of slots: grid (chunk, head).  A warp
 // takes every eighth 16 slots of the chunk, the next ones in flight; the
-// running (max, sum) of a row stays in the lanes that hold its column.
-template <class Tag, int NB, int NT>
+// running (max, sum) of a row stays in the four lanes that hold it.
+template <class Tag, int NB, int MT>
 __global__ void __launch_bounds__(kScoreThreads, 2) k_score_few(const __grid_constant__ ScoreArgs a)
 {
     extern __shared__ __align__(16) unsigned char smem[];
     uint4 *sq = reinterpret_cast<uint4 *>(smem);
-    __shared__ float2 stat[kScoreWarps][8 * NT];
+    __shared__ float2 stat[kScoreWarps][16 * MT];
     const int64_t head = blockIdx.y;
     const int b = static_cast<int>(head / a.H), h = static_cast<int>(head % a.H);
     const Span sp = span_of(a, b);
@@ -448,59 +476,67 @@ __global__ void __launch_bounds__(kScoreThreads, 2) k_score_few(const __grid_con
     const int t_begin = blockIdx.x * a.part, t_end = min(sp.end, t_begin + a.part);
     if (!sp.ok || rows == 0 || t_begin >= t_end) return;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t2 = 2 * (lane & 3);
-    const int nb = (a.D + 31) / 32, tiles = (rows + 7) / 8;
+    const int nb = (a.D + 31) / 32, tiles = (rows + 15) / 16;
     const auto *keys = static_cast<const typename Tag::elem *>(a.k) + b * a.k_req + h * a.k_head;
-    float *products_out = a.held + head * a.R * a.pitch;
+    float *held = a.held + head * a.R * a.pitch;
     Slots<Tag, NB> cur, next;
     int t0 = t_begin + warp * 16;
     if (t0 < t_end) cur.load(a, keys, t0, t_end);
     stage_rows<Tag>(a, b, h, 0, rows, tiles, nb, sq);
     __syncthreads();
-    float m[NT][2], l[NT][2];
+    float m[MT][2], l[MT][2];
 #pragma unroll
-    for (int n = 0; n < NT; ++n) m[n][0] = m[n][1] = -INFINITY, l[n][0] = l[n][1] = 0.f;
+    for (int i = 0; i < MT; ++i) m[i][0] = m[i][1] = -INFINITY, l[i][0] = l[i][1] = 0.f;
     for (; t0 < t_end; t0 += kScoreWarps * 16) {
         if (t0 + kScoreWarps * 16 < t_end) next.load(a, keys, t0 + kScoreWarps * 16, t_end);
-        float c[NT][4];
-        products<Tag, NB, NT>(cur, sq, nb, 0, tiles, c);
+        float c[MT][2][4];
+        products<Tag, NB, MT>(cur, sq, nb, 0, tiles, c);
         const bool whole = t0 + 16 <= min(t_end, sp.begin + 1);
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
+        for (int i = 0; i < MT; ++i)
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const int r = n * 8 + t2 + e;
+            for (int low = 0; low < 2; ++low) {
+                const int r = 16 * i + g + 8 * low;
                 if (r < rows) {
-                    float x[2];
+                    float x[4];  // slots t0 + t2, + 1, + 8, + 9
 #pragma unroll
-                    for (int half = 0; half < 2; ++half) {
-                        const int t = t0 + g + 8 * half;
-                        x[half] = __fmul_rn(c[n][2 * half + e], a.scale2);
-                        if (!whole && !(t < t_end && t <= sp.begin + r / a.G)) x[half] = -INFINITY;
-                        if (whole || t < t_end) products_out[static_cast<int64_t>(r) * a.pitch + t] = x[half];
+                    for (int e = 0; e < 4; ++e) x[e] = __fmul_rn(c[i][e >> 1][2 * low + (e & 1)], a.scale2);
+                    float *to = held + static_cast<int64_t>(r) * a.pitch + t0 + t2;
+                    if (whole) {
+                        *reinterpret_cast<float2 *>(to) = make_float2(x[0], x[1]);
+                        *reinterpret_cast<float2 *>(to + 8) = make_float2(x[2], x[3]);
+                    } else {
+                        const int last = sp.begin + r / a.G;
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const int at = (e >> 1) * 8 + (e & 1), t = t0 + t2 + at;
+                            if (!(t < t_end && t <= last)) x[e] = -INFINITY;
+                            if (t < t_end) to[at] = x[e];
+                        }
                     }
-                    const float top = fmaxf(x[0], x[1]);
-                    if (top > m[n][e]) {
-                        l[n][e] *= ex2_approx(m[n][e] - top);
-                        m[n][e] = top;
+                    const float top = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
+                    if (top > m[i][low]) {
+                        l[i][low] *= ex2_approx(m[i][low] - top);
+                        m[i][low] = top;
                     }
-                    const float mm = m[n][e] == -INFINITY ? 0.f : m[n][e];
-                    l[n][e] += ex2_approx(x[0] - mm) + ex2_approx(x[1] - mm);
+                    const float mm = m[i][low] == -INFINITY ? 0.f : m[i][low];
+                    l[i][low] += (ex2_approx(x[0] - mm) + ex2_approx(x[1] - mm)) + (ex2_approx(x[2] - mm) + ex2_approx(x[3] - mm));
                 }
             }
         cur = next;
     }
 #pragma unroll
-    for (int n = 0; n < NT; ++n)
+    for (int i = 0; i < MT; ++i)
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            float mm = m[n][e], ll = l[n][e];
+        for (int low = 0; low < 2; ++low) {
+            float mm = m[i][low], ll = l[i][low];
 #pragma unroll
-            for (int o = 4; o < 32; o <<= 1) {
+            for (int o = 1; o < 4; o <<= 1) {
                 const float om = __shfl_xor_sync(kFull, mm, o), ol = __shfl_xor_sync(kFull, ll, o);
                 merge(mm, ll, om, ol);
                 if (ol != ol) ll = ol;
             }
-            if (g == 0) stat[warp][n * 8 + t2 + e] = make_float2(mm, ll);
+            if (t2 == 0) stat[warp][16 * i + g + 8 * low] = make_float2(mm, ll);
         }
     __syncthreads();
     if (threadIdx.x < rows) {
@@ -589,15 +625,16 @@ __global__ void __launch_bounds__(kScoreThreads) k_score_sum(const __grid_consta
 // --------------------------------------------------------- many rows (bf16)
 // Where a key head has many rows (a prompt's last queries, a verification with
 // wide groups) the products no longer fit shared memory and the exponentials
-// and the tensor pipe bound the step, not the keys.  Two kernels, no cluster
+// and the tensor pipe bound the step, not the keys.  Two sweeps, no cluster
 // (16 blocks of one SM each fit only some of the processing clusters, and
 // eight would leave SMs idle):
-//   k_score_rows   a warp holds 16 * MR rows as A fragments, the keys stream
-//                  through shared memory as B fragments for all warps; the
-//                  running (max, sum) of a row stays in its four lanes;
-//   k_score_slots  a warp holds 32 slots as A fragments, the rows are B
-//                  fragments in shared memory; a slot's sum over the rows
-//                  stays in its four lanes.
+//   k_score_rows   a warp holds 16 * MR rows as A fragments in registers, the keys
+//                  stream through shared memory as B fragments for all warps; the
+//                  running (max, sum) of a row stays in its four lanes (its
+//                  chunks are merged by k_score_merge);
+//   k_score_slots  a warp holds 32 slots as B fragments in registers, the rows
+//                  are A fragments in shared memory; a slot's sum over the
+//                  rows stays in the eight lanes of its column.
 // tcgen05 accumulators were built and measured for this step: they would
 // halve its time, but drop what falls below the running sum at each of the
 // D / 16 steps, and the weights came out 6e-6 off (2-norm, against 3e-7 here)
@@ -646,29 +683,28 @@ __global__ void __launch_bounds__(kScoreThreads, 2) k_score_rows(const __grid_co
     const auto *keys = static_cast<const uint16_t *>(a.k) + b * a.k_req + h * a.k_head;
     const int stage_slots = row_slots * groups, stage = stage_slots / 8 * NB * 32;  // uint4
     const int stages = (t_end - t_begin + stage_slots - 1) / stage_slots;
+    // this warp's rows, by way of the ring: lane (g, t) holds rows g and g + 8
+    // of each 16
+    stage_rows<Bf16>(a, b, h, r0, rows, (nr + 15) / 16, NB, ring);
+    __syncthreads();
+    uint4 q[MR][NB][2];
+    int last[MR][2];  // the last slot a row sees
+#pragma unroll
+    for (int i = 0; i < MR; ++i) {
+        const bool in = rw + 16 * i < nr;
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            last[i][half] = sp.begin + (r0 + rw + 16 * i + g + 8 * half) / a.G;
+#pragma unroll
+            for (int j = 0; j < NB; ++j)
+                q[i][j][half] = in ? ring[((rw / 16 + i) * NB + j) * 64 + half * 32 + lane] : make_uint4(0u, 0u, 0u, 0u);
+        }
+    }
+    __syncthreads();
     for (int s = 0; s < kRowStages - 1; ++s) {
         if (s < stages) copy_slots<NB>(a, keys, t_begin + s * stage_slots, stage_slots, t_end, ring + s * stage);
         asm volatile("cp.async.commit_group;\n" ::: "memory");
     }
-    // this warp's rows: lane (g, t) holds rows g and g + 8 of each 16
-    uint4 q[MR][NB][2];
-    int last[MR][2];  // the last slot a row sees
-#pragma unroll
-    for (int i = 0; i < MR; ++i)
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-            const int r = r0 + rw + 16 * i + g + 8 * half;
-            const int qi = r / a.G, x = r - qi * a.G;
-            last[i][half] = sp.begin + qi;
-            const auto *row = static_cast<const uint16_t *>(a.q) + b * a.q_req + qi * a.q_tok +
-                              (static_cast<int64_t>(h) * a.G + x) * a.q_head;
-#pragma unroll
-            for (int j = 0; j < NB; ++j) {
-                uint4 raw[1];
-                load8<Bf16>(row, r < rows ? 32 * j + 8 * t : a.D, a.D, raw);
-                q[i][j][half] = raw[0];
-            }
-        }
     float m[MR][2], l[MR][2];  // of this lane's columns, m in units of log2
 #pragma unroll
     for (int i = 0; i < MR; ++i) m[i][0] = m[i][1] = -INFINITY, l[i][0] = l[i][1] = 0.f;
@@ -685,9 +721,9 @@ __global__ void __launch_bounds__(kScoreThreads, 2) k_score_rows(const __grid_co
 #pragma unroll
                 for (int i = 0; i < MR; ++i) {
                     const uint4 u = q[i][j][0], v = q[i][j][1];
-                    if (j == 0) mma_bf16_first(c[n][i], u.x, v.x, u.y, v.y, w.x, w.y);
-                    else mma_bf16(c[n][i], u.x, v.x, u.y, v.y, w.x, w.y);
-                    mma_bf16(c[n][i], u.z, v.z, u.w, v.w, w.z, w.w);
+                    if (j == 0) mma_bf16_first(c[n][i], u.x, u.y, u.z, u.w, w.x, w.y);
+                    else mma_bf16(c[n][i], u.x, u.y, u.z, u.w, w.x, w.y);
+                    mma_bf16(c[n][i], v.x, v.y, v.z, v.w, w.z, w.w);
                 }
             }
 #pragma unroll
@@ -770,11 +806,38 @@ __global__ void __launch_bounds__(kScoreThreads, 2) k_score_rows(const __grid_co
     }
 }
 
+// -L of every row from its chunks' statistics: a warp a row.
+__global__ void __launch_bounds__(kScoreThreads) k_score_merge(const __grid_constant__ ScoreArgs a)
+{
+    const int lane = threadIdx.x & 31;
+    const int64_t row = (static_cast<int64_t>(blockIdx.x) * kScoreThreads + threadIdx.x) >> 5;
+    asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
+    if (row >= static_cast<int64_t>(a.B) * a.H * a.R) return;
+    const Span sp = span_of(a, static_cast<int>(row / (static_cast<int64_t>(a.H) * a.R)));
+    asm volatile("griddepcontrol.wait;\n" ::: "memory");
+    if (!sp.ok || row % a.R >= (sp.end - sp.begin) * a.G) return;
+    const int chunks = (sp.end + a.part - 1) / a.part;
+    float m = -INFINITY, l = 0.f;
+#pragma unroll 2
+    for (int c = lane; c < chunks; c += 32) {
+        const float2 y = __ldcg(a.stats + row * a.chunks + c);
+        merge(m, l, y.x, y.y);
+        if (y.y != y.y) l = y.y;
+    }
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const float om = __shfl_xor_sync(kFull, m, o), ol = __shfl_xor_sync(kFull, l, o);
+        merge(m, l, om, ol);
+        if (ol != ol) l = ol;
+    }
+    if (lane == 0) __stcg(a.minus_l + row, -(m + log2f(l)));
+}
+
 // The weights of one chunk of slots: grid (chunk, request and head).
 template <int NB>
 __global__ void __launch_bounds__(kScoreThreads, 2) k_score_slots(const __grid_constant__ ScoreArgs a)
 {
-    constexpr int kM = NB <= 4 ? 2 : 1;  // m-tiles of 16 slots a warp
+    constexpr int kN = NB <= 4 ? 4 : 2;  // tiles of 8 slots a warp
     extern __shared__ __align__(16) unsigned char smem[];
     uint4 *sq = reinterpret_cast<uint4 *>(smem);
     __shared__ __align__(8) float minus_l[kManyRows];
@@ -793,102 +856,94 @@ __global__ void __launch_bounds__(kScoreThreads, 2) k_score_slots(const __grid_c
     const float *in = a.in + head * a.C;
     float *out = a.out + head * a.C;
     const float sc = a.scale2;
-    const int chunks = (sp.end + a.part - 1) / a.part;
     for (int r0 = 0; r0 < max(rows, 1); r0 += kManyRows) {
-        const int nr = min(rows - r0, kManyRows), tiles = (nr + 7) / 8;
+        const int nr = min(rows - r0, kManyRows), tiles = (nr + 15) / 16;
         __syncthreads();
         stage_rows<Bf16>(a, b, h, r0, rows, tiles, NB, sq);
         if (r0 == 0) asm volatile("griddepcontrol.wait;\n" ::: "memory");
-        // eight lanes a row merge the chunks' statistics
-        for (int i = threadIdx.x; i < tiles * 64; i += kScoreThreads) {
-            const int r = i >> 3;
-            float mm = -INFINITY, ll = 0.f;
-            if (r < nr)
-                for (int c = i & 7; c < chunks; c += 8) {
-                    const float2 y = __ldcg(a.stats + (head * a.R + r0 + r) * a.chunks + c);
-                    merge(mm, ll, y.x, y.y);
-                    if (y.y != y.y) ll = y.y;
-                }
-#pragma unroll
-            for (int o = 1; o < 8; o <<= 1) {
-                const float om = __shfl_xor_sync(kFull, mm, o), ol = __shfl_xor_sync(kFull, ll, o);
-                merge(mm, ll, om, ol);
-                if (ol != ol) ll = ol;
-            }
-            // a row that is none weighs nothing
-            if ((i & 7) == 0) minus_l[r] = r < nr ? -(mm + log2f(ll)) : -INFINITY;
-        }
+        // a row that is none weighs nothing
+        for (int r = threadIdx.x; r < tiles * 16; r += kScoreThreads)
+            minus_l[r] = r < nr ? __ldcg(a.minus_l + head * a.R + r0 + r) : -INFINITY;
         __syncthreads();
-        for (int t0 = t_begin + warp * 16 * kM; t0 < t_end; t0 += kScoreWarps * 16 * kM) {
-            uint4 k[kM][NB][2];
-            float old[kM][2];
-            unsigned long long sum[kM][2];  // of this lane's even and odd rows
-            int first[kM][2];               // the first row that sees the slot
+        for (int t0 = t_begin + warp * 8 * kN; t0 < t_end; t0 += kScoreWarps * 8 * kN) {
+            uint4 k[kN][NB];  // lane (g, t): elements 32 j + 8 t .. + 7 of slot g of each 8
 #pragma unroll
-            for (int i = 0; i < kM; ++i)
-#pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                    const int slot = t0 + 16 * i + g + 8 * half;
-                    const auto *row = keys + slot * a.k_slot;
-#pragma unroll
-                    for (int j = 0; j < NB; ++j) {
-                        uint4 raw[1];
-                        load8<Bf16>(row, slot < t_end ? 32 * j + 8 * t : a.D, a.D, raw);
-                        k[i][j][half] = raw[0];
-                    }
-                    old[i][half] = t != 0 || slot >= t_end ? 0.f : r0 > 0 ? out[slot] : slot < sp.begin ? in[slot] : 0.f;
-                    sum[i][half] = f2_pack(0.f, 0.f);
-                    first[i][half] = max(0, (slot - sp.begin) * a.G - r0);
-                }
-            // rows 8 n .. 8 n + 7; `whole`: the slots are seen by every row
-            auto step = [&](int n, auto whole) {
-                float c[kM][4];
+            for (int n = 0; n < kN; ++n) {
+                const int slot = t0 + 8 * n + g;
+                const auto *row = keys + slot * a.k_slot;
 #pragma unroll
                 for (int j = 0; j < NB; ++j) {
-                    const uint4 w = sq[(n * NB + j) * 32 + lane];
-#pragma unroll
-                    for (int i = 0; i < kM; ++i) {
-                        const uint4 u = k[i][j][0], v = k[i][j][1];
-                        if (j == 0) mma_bf16_first(c[i], u.x, v.x, u.y, v.y, w.x, w.y);
-                        else mma_bf16(c[i], u.x, v.x, u.y, v.y, w.x, w.y);
-                        mma_bf16(c[i], u.z, v.z, u.w, v.w, w.z, w.w);
-                    }
+                    uint4 raw[1];
+                    load8<Bf16>(row, slot < t_end ? 32 * j + 8 * t : a.D, a.D, raw);
+                    k[n][j] = raw[0];
                 }
-                const unsigned long long y = *reinterpret_cast<const unsigned long long *>(&minus_l[n * 8 + 2 * t]);
+            }
+            // lane (g, t) writes slots 2 t, 2 t + 1 of tile g
+            const int mine = t0 + 8 * g + 2 * t;
+            float old[2];
 #pragma unroll
-                for (int i = 0; i < kM; ++i)
+            for (int e = 0; e < 2; ++e)
+                old[e] = g >= kN || mine + e >= t_end ? 0.f : r0 > 0 ? out[mine + e] : mine + e < sp.begin ? in[mine + e] : 0.f;
+            unsigned long long sum[kN];  // slots 2 t, 2 t + 1 of each tile, this lane's rows
 #pragma unroll
-                    for (int half = 0; half < 2; ++half) {
-                        unsigned long long z = f2_add(f2_pack(__fmul_rn(c[i][2 * half], sc), __fmul_rn(c[i][2 * half + 1], sc)), y);
-                        if (!whole) {
+            for (int n = 0; n < kN; ++n) sum[n] = f2_pack(0.f, 0.f);
+            // rows 16 x .. 16 x + 15; `whole`: the slots are seen by every row
+            auto step = [&](int x, auto whole) {
+                float c[kN][4];
+#pragma unroll
+                for (int j = 0; j < NB; ++j) {
+                    const uint4 u = sq[(x * NB + j) * 64 + lane], v = sq[(x * NB + j) * 64 + 32 + lane];
+#pragma unroll
+                    for (int n = 0; n < kN; ++n) {
+                        if (j == 0) mma_bf16_first(c[n], u.x, u.y, u.z, u.w, k[n][j].x, k[n][j].y);
+                        else mma_bf16(c[n], u.x, u.y, u.z, u.w, k[n][j].x, k[n][j].y);
+                    }
+#pragma unroll
+                    for (int n = 0; n < kN; ++n) mma_bf16(c[n], v.x, v.y, v.z, v.w, k[n][j].z, k[n][j].w);
+                }
+#pragma unroll
+                for (int low = 0; low < 2; ++low) {
+                    const int r = 16 * x + g + 8 * low;
+                    const float y = minus_l[r];
+                    const unsigned long long y2 = f2_pack(y, y);
+#pragma unroll
+                    for (int n = 0; n < kN; ++n) {
+                        unsigned long long z =
+                            f2_add(f2_pack(__fmul_rn(c[n][2 * low], sc), __fmul_rn(c[n][2 * low + 1], sc)), y2);
+                        if (!whole) {  // the first row that sees a slot
                             float z0, z1;
                             f2_unpack(z, z0, z1);
-                            if (n * 8 + 2 * t < first[i][half]) z0 = -INFINITY;
-                            if (n * 8 + 2 * t + 1 < first[i][half]) z1 = -INFINITY;
+                            const int first = (t0 + 8 * n + 2 * t - sp.begin) * a.G - r0;
+                            if (r < first) z0 = -INFINITY;
+                            if (r < first + a.G) z1 = -INFINITY;
                             z = f2_pack(z0, z1);
                         }
-                        sum[i][half] = f2_add(sum[i][half], f2_ex2(z));
+                        sum[n] = f2_add(sum[n], f2_ex2(z));
                     }
+                }
             };
-            if (t0 + 16 * kM <= sp.begin + 1) {
-#pragma unroll 2
-                for (int n = 0; n < tiles; ++n) step(n, std::true_type{});
+            if (t0 + 8 * kN <= sp.begin + 1) {
+#pragma unroll 1
+                for (int x = 0; x < tiles; ++x) step(x, std::true_type{});
             } else {
 #pragma unroll 1
-                for (int n = 0; n < tiles; ++n) step(n, std::false_type{});
+                for (int x = 0; x < tiles; ++x) step(x, std::false_type{});
+            }
+            float add[2] = {0.f, 0.f};
+#pragma unroll
+            for (int n = 0; n < kN; ++n) {
+                float x0, x1;
+                f2_unpack(sum[n], x0, x1);
+#pragma unroll
+                for (int o = 4; o < 32; o <<= 1) {
+                    x0 += __shfl_xor_sync(kFull, x0, o);
+                    x1 += __shfl_xor_sync(kFull, x1, o);
+                }
+                if (g == n) add[0] = x0, add[1] = x1;
             }
 #pragma unroll
-            for (int i = 0; i < kM; ++i)
-#pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                    float x, x1;
-                    f2_unpack(sum[i][half], x, x1);
-                    x += x1;
-                    x += __shfl_xor_sync(kFull, x, 1);
-                    x += __shfl_xor_sync(kFull, x, 2);
-                    const int slot = t0 + 16 * i + g + 8 * half;
-                    if (t == 0 && slot < t_end) out[slot] = old[i][half] + x;
-                }
+            for (int e = 0; e < 2; ++e)
+                if (g < kN && mine + e < t_end) out[mine + e] = old[e] + add[e];
         }
     }
 }
@@ -909,9 +964,9 @@ ScorePlan score_plan(int B, int H, int R, int D, int C, bool f32)
     ScorePlan p;
     // rows of a tile: their fragments, statistics and at least kPartSlots products
     const int64_t row_bytes = ceil_div(D, 32) * 64 * (f32 ? 3 : 1) + 4 * (kPartSlots + 36) + 12;
-    const int64_t most = std::min<int64_t>(128, (kScoreSmem - 96) / row_bytes / 8 * 8);
+    const int64_t most = std::min<int64_t>(128, (kScoreSmem - 96) / row_bytes / 16 * 16);
     const int64_t tiles = ceil_div(R, most);
-    p.tile_rows = static_cast<int>(ceil_div(ceil_div(R, tiles), 8) * 8);
+    p.tile_rows = static_cast<int>(ceil_div(ceil_div(R, tiles), 16) * 16);
     p.held_rows = std::min(R, p.tile_rows);
     const size_t frag = static_cast<size_t>(p.tile_rows) * ceil_div(D, 32) * 64 * (f32 ? 3 : 1);
     const size_t stat = static_cast<size_t>(std::max(p.tile_rows, kScoreWarps)) * 12;
@@ -989,26 +1044,26 @@ FewPlan few_plan(int B, int H, int R, int C)
     return p;
 }
 
-bool g_few_attr[64][2][3][3];
+bool g_few_attr[64][2][3][2];
 
-template <class Tag, int NB, int NT>
-int launch_few(const ScoreArgs &a, int dtype_index, int nb_index, int nt_index, cudaStream_t st)
+template <class Tag, int NB, int MT>
+int launch_few(const ScoreArgs &a, int dtype_index, int nb_index, int mt_index, cudaStream_t st)
 {
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return SPEC_ECUDA;
     const int nb = (a.D + 31) / 32;
-    const size_t smem = static_cast<size_t>(ceil_div(a.R, 8)) * nb * 512 * Parts<Tag>::kParts;
+    const size_t smem = static_cast<size_t>(ceil_div(a.R, 16)) * nb * 1024 * Parts<Tag>::kParts;
     {
         std::lock_guard<std::mutex> lock(g_score_mu);
-        if (!g_few_attr[dev][dtype_index][nb_index][nt_index]) {
-            if (cudaFuncSetAttribute(k_score_few<Tag, NB, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                     NT * NB * 512 * Parts<Tag>::kParts) != cudaSuccess)
+        if (!g_few_attr[dev][dtype_index][nb_index][mt_index]) {
+            if (cudaFuncSetAttribute(k_score_few<Tag, NB, MT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                     MT * NB * 1024 * Parts<Tag>::kParts) != cudaSuccess)
                 return SPEC_ECUDA;
-            g_few_attr[dev][dtype_index][nb_index][nt_index] = true;
+            g_few_attr[dev][dtype_index][nb_index][mt_index] = true;
         }
     }
     const unsigned heads = static_cast<unsigned>(a.B * a.H);
-    k_score_few<Tag, NB, NT><<<dim3(static_cast<unsigned>(a.chunks), heads), kScoreThreads, smem, st>>>(a);
+    k_score_few<Tag, NB, MT><<<dim3(static_cast<unsigned>(a.chunks), heads), kScoreThreads, smem, st>>>(a);
     if (cudaGetLastError() != cudaSuccess) return SPEC_ECUDA;
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];
@@ -1028,9 +1083,8 @@ int launch_few(const ScoreArgs &a, int dtype_index, int nb_index, int nt_index, 
 template <class Tag, int NB>
 int launch_few(const ScoreArgs &a, int dtype_index, int nb_index, cudaStream_t st)
 {
-    if (a.R <= 8) return launch_few<Tag, NB, 1>(a, dtype_index, nb_index, 0, st);
-    if (a.R <= 16) return launch_few<Tag, NB, 2>(a, dtype_index, nb_index, 1, st);
-    return launch_few<Tag, NB, 4>(a, dtype_index, nb_index, 2, st);
+    return a.R <= 16 ? launch_few<Tag, NB, 1>(a, dtype_index, nb_index, 0, st)
+                     : launch_few<Tag, NB, 2>(a, dtype_index, nb_index, 1, st);
 }
 template <class Tag>
 int launch_few(const ScoreArgs &a, int dtype_index, cudaStream_t st)
@@ -1044,7 +1098,7 @@ int launch_few(const ScoreArgs &a, int dtype_index, cudaStream_t st)
 // step: about two blocks a SM for each, in whole stages.
 struct ManyPlan {
     int part, chunks, slots;
-    size_t stats_bytes;
+    size_t stats_bytes, l_bytes;
 };
 ManyPlan many_plan(int B, int H, int R, int C)
 {
@@ -1055,7 +1109,8 @@ ManyPlan many_plan(int B, int H, int R, int C)
     p.chunks = static_cast<int>(ceil_div(C, p.part));
     const int64_t blocks = std::max<int64_t>(1, 2 * 148 / heads);
     p.slots = static_cast<int>(ceil_div(ceil_div(C, blocks), 256) * 256);
-    p.stats_bytes = sizeof(float2) * static_cast<size_t>(heads) * R * p.chunks;
+    p.stats_bytes = align_up(sizeof(float2) * static_cast<size_t>(heads) * R * p.chunks);
+    p.l_bytes = align_up(sizeof(float) * static_cast<size_t>(heads) * R);
     return p;
 }
 
@@ -1097,9 +1152,18 @@ int launch_many(ScoreArgs a, int nb_index, cudaStream_t st)
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.gridDim = dim3(static_cast<unsigned>(ceil_div(static_cast<int64_t>(heads) * a.R, kScoreWarps)));
+    cfg.blockDim = dim3(kScoreThreads);
+    cfg.stream = st;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaLaunchKernelEx(&cfg, k_score_merge, a) != cudaSuccess) {
+        (void)cudaGetLastError();
+        return SPEC_ECUDA;
+    }
     cfg.gridDim = dim3(static_cast<unsigned>(ceil_div(a.C, a.slots)), heads);
     cfg.blockDim = dim3(kScoreThreads);
-    cfg.dynamicSmemBytes = ceil_div(top, 8) * NB * 512;
+    cfg.dynamicSmemBytes = ceil_div(top, 16) * NB * 1024;
     cfg.stream = st;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
@@ -1136,7 +1200,8 @@ extern "C" size_t spec_score_workspace_size(int batch, int queries, int q_heads,
         const FewPlan p = few_plan(B, kv_heads, R, capacity);
         n = std::max(n, p.stats_bytes + p.held_bytes);
     }
-    return std::max(n, align_up(many_plan(B, kv_heads, R, capacity).stats_bytes));
+    const ManyPlan p = many_plan(B, kv_heads, R, capacity);
+    return std::max(n, p.stats_bytes + p.l_bytes);
 }
 
 extern "C" int spec_cache_score(const void *q, const void *k, spec_dtype_t dtype, int64_t q_request_stride,
@@ -1209,6 +1274,7 @@ extern "C" int spec_cache_score(const void *q, const void *k, spec_dtype_t dtype
         a.part = many.part;
         a.chunks = many.chunks;
         a.slots = many.slots;
+        a.minus_l = reinterpret_cast<float *>(static_cast<char *>(workspace) + many.stats_bytes);
         if (head_dim <= 64) return launch_many<2, 2>(a, 0, stream);
         if (head_dim <= 128) return launch_many<4, 2>(a, 1, stream);
         return launch_many<8, 1>(a, 2, stream);

@@ -628,7 +628,7 @@ __global__ void __launch_bounds__(kScoreThreads) k_score_sum(const __grid_consta
 // and the tensor pipe bound the step, not the keys.  Two sweeps, no cluster
 // (16 blocks of one SM each fit only some of the processing clusters, and
 // eight would leave SMs idle):
-//   k_score_rows   a warp holds 16 * MR rows as A fragments in registers, the keys
+//   k_score_rows   a warp holds 16 rows as A fragments in registers, the keys
 //                  stream through shared memory as B fragments for all warps; the
 //                  running (max, sum) of a row stays in its four lanes (its
 //                  chunks are merged by k_score_merge);
@@ -661,12 +661,12 @@ __device__ __forceinline__ void copy_slots(const ScoreArgs &a, const uint16_t *k
 
 // Statistics of the rows of one tile over one chunk of slots: grid (chunk,
 // row tile, request and head).
-template <int NB, int MR>
+template <int NB>
 __global__ void __launch_bounds__(kScoreThreads, 2) k_score_rows(const __grid_constant__ ScoreArgs a)
 {
     extern __shared__ __align__(16) unsigned char smem[];
     uint4 *ring = reinterpret_cast<uint4 *>(smem);
-    __shared__ float2 stat[kScoreWarps][16 * MR];
+    __shared__ float2 stat[kScoreWarps][16];
     const int64_t head = blockIdx.z;
     const int b = static_cast<int>(head / a.H), h = static_cast<int>(head % a.H);
     const Span sp = span_of(a, b);
@@ -676,10 +676,10 @@ __global__ void __launch_bounds__(kScoreThreads, 2) k_score_rows(const __grid_co
     if (!sp.ok || r0 >= rows || t_begin >= t_end) return;
     const int nr = min(rows - r0, kManyRows);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
-    const int wr = (min(a.R, kManyRows) + 16 * MR - 1) / (16 * MR);  // warps over the rows
+    const int wr = (min(a.R, kManyRows) + 15) / 16;  // warps over the rows
     const int groups = (blockDim.x >> 5) / wr;                          // groups of them over the slots
     const int row_slots = a.slots;                                      // of a stage, for each group
-    const int rw = (warp % wr) * 16 * MR, sg = warp / wr;
+    const int rw = (warp % wr) * 16, sg = warp / wr;
     const auto *keys = static_cast<const uint16_t *>(a.k) + b * a.k_req + h * a.k_head;
     const int stage_slots = row_slots * groups, stage = stage_slots / 8 * NB * 32;  // uint4
     const int stages = (t_end - t_begin + stage_slots - 1) / stage_slots;
@@ -687,78 +687,67 @@ __global__ void __launch_bounds__(kScoreThreads, 2) k_score_rows(const __grid_co
     // of each 16
     stage_rows<Bf16>(a, b, h, r0, rows, (nr + 15) / 16, NB, ring);
     __syncthreads();
-    uint4 q[MR][NB][2];
-    int last[MR][2];  // the last slot a row sees
+    uint4 q[NB][2];
+    int last[2];  // the last slot a row sees
 #pragma unroll
-    for (int i = 0; i < MR; ++i) {
-        const bool in = rw + 16 * i < nr;
+    for (int half = 0; half < 2; ++half) {
+        last[half] = sp.begin + (r0 + rw + g + 8 * half) / a.G;
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-            last[i][half] = sp.begin + (r0 + rw + 16 * i + g + 8 * half) / a.G;
-#pragma unroll
-            for (int j = 0; j < NB; ++j)
-                q[i][j][half] = in ? ring[((rw / 16 + i) * NB + j) * 64 + half * 32 + lane] : make_uint4(0u, 0u, 0u, 0u);
-        }
+        for (int j = 0; j < NB; ++j)
+            q[j][half] = rw < nr ? ring[(rw / 16 * NB + j) * 64 + half * 32 + lane] : make_uint4(0u, 0u, 0u, 0u);
     }
     __syncthreads();
     for (int s = 0; s < kRowStages - 1; ++s) {
         if (s < stages) copy_slots<NB>(a, keys, t_begin + s * stage_slots, stage_slots, t_end, ring + s * stage);
         asm volatile("cp.async.commit_group;\n" ::: "memory");
     }
-    float m[MR][2], l[MR][2];  // of this lane's columns, m in units of log2
-#pragma unroll
-    for (int i = 0; i < MR; ++i) m[i][0] = m[i][1] = -INFINITY, l[i][0] = l[i][1] = 0.f;
+    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};  // of this lane's columns, m in units of log2
     const float sc = a.scale2;
 
     // 32 slots from t0 on, as fragments at `tile`; `whole`: seen by every row
     auto step = [&](const uint4 *tile, int t0, auto whole) {
-        float c[4][MR][4];
+        float c[4][4];
 #pragma unroll
         for (int j = 0; j < NB; ++j)
 #pragma unroll
             for (int n = 0; n < 4; ++n) {
                 const uint4 w = tile[(n * NB + j) * 32];
-#pragma unroll
-                for (int i = 0; i < MR; ++i) {
-                    const uint4 u = q[i][j][0], v = q[i][j][1];
-                    if (j == 0) mma_bf16_first(c[n][i], u.x, u.y, u.z, u.w, w.x, w.y);
-                    else mma_bf16(c[n][i], u.x, u.y, u.z, u.w, w.x, w.y);
-                    mma_bf16(c[n][i], v.x, v.y, v.z, v.w, w.z, w.w);
-                }
+                const uint4 u = q[j][0], v = q[j][1];
+                if (j == 0) mma_bf16_first(c[n], u.x, u.y, u.z, u.w, w.x, w.y);
+                else mma_bf16(c[n], u.x, u.y, u.z, u.w, w.x, w.y);
+                mma_bf16(c[n], v.x, v.y, v.z, v.w, w.z, w.w);
             }
 #pragma unroll
-        for (int i = 0; i < MR; ++i)
+        for (int half = 0; half < 2; ++half) {
+            // the scaled products are rounded here and in k_score_slots
+            // alike: fused, they would differ from L's by half a step of s
+            float x[8];
 #pragma unroll
-            for (int half = 0; half < 2; ++half) {
-                // the scaled products are rounded here and in k_score_slots
-                // alike: fused, they would differ from L's by half a step of s
-                float x[8];
+            for (int n = 0; n < 4; ++n)
+                x[2 * n] = __fmul_rn(c[n][2 * half], sc), x[2 * n + 1] = __fmul_rn(c[n][2 * half + 1], sc);
+            if (!whole) {
 #pragma unroll
-                for (int n = 0; n < 4; ++n)
-                    x[2 * n] = __fmul_rn(c[n][i][2 * half], sc), x[2 * n + 1] = __fmul_rn(c[n][i][2 * half + 1], sc);
-                if (!whole) {
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        const int slot = t0 + (e >> 1) * 8 + 2 * t + (e & 1);
-                        if (!(slot < t_end && slot <= last[i][half])) x[e] = -INFINITY;
-                    }
+                for (int e = 0; e < 8; ++e) {
+                    const int slot = t0 + (e >> 1) * 8 + 2 * t + (e & 1);
+                    if (!(slot < t_end && slot <= last[half])) x[e] = -INFINITY;
                 }
-                float top = x[0];
-#pragma unroll
-                for (int e = 1; e < 8; ++e) top = fmaxf(top, x[e]);
-                if (top > m[i][half]) {
-                    l[i][half] *= ex2_approx(m[i][half] - top);
-                    m[i][half] = top;
-                }
-                const float mm = !whole && m[i][half] == -INFINITY ? 0.f : m[i][half];
-                const unsigned long long nm = f2_pack(-mm, -mm);
-                unsigned long long e01 = f2_ex2(f2_add(f2_pack(x[0], x[1]), nm));
-#pragma unroll
-                for (int n = 1; n < 4; ++n) e01 = f2_add(e01, f2_ex2(f2_add(f2_pack(x[2 * n], x[2 * n + 1]), nm)));
-                float e0, e1;
-                f2_unpack(e01, e0, e1);
-                l[i][half] += e0 + e1;
             }
+            float top = x[0];
+#pragma unroll
+            for (int e = 1; e < 8; ++e) top = fmaxf(top, x[e]);
+            if (top > m[half]) {
+                l[half] *= ex2_approx(m[half] - top);
+                m[half] = top;
+            }
+            const float mm = !whole && m[half] == -INFINITY ? 0.f : m[half];
+            const unsigned long long nm = f2_pack(-mm, -mm);
+            unsigned long long e01 = f2_ex2(f2_add(f2_pack(x[0], x[1]), nm));
+#pragma unroll
+            for (int n = 1; n < 4; ++n) e01 = f2_add(e01, f2_ex2(f2_add(f2_pack(x[2 * n], x[2 * n + 1]), nm)));
+            float e0, e1;
+            f2_unpack(e01, e0, e1);
+            l[half] += e0 + e1;
+        }
     };
     for (int s = 0; s < stages; ++s) {
         asm volatile("cp.async.wait_group %0;\n" ::"n"(kRowStages - 2) : "memory");
@@ -782,23 +771,21 @@ __global__ void __launch_bounds__(kScoreThreads, 2) k_score_rows(const __grid_co
     }
     asm volatile("cp.async.wait_group 0;\n" ::: "memory");
 #pragma unroll
-    for (int i = 0; i < MR; ++i)
+    for (int half = 0; half < 2; ++half) {
+        float mm = m[half], ll = l[half];
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-            float mm = m[i][half], ll = l[i][half];
-#pragma unroll
-            for (int o = 1; o < 4; o <<= 1) {
-                const float om = __shfl_xor_sync(kFull, mm, o), ol = __shfl_xor_sync(kFull, ll, o);
-                merge(mm, ll, om, ol);
-                if (ol != ol) ll = ol;
-            }
-            if (t == 0) stat[warp][16 * i + g + 8 * half] = make_float2(mm, ll);
+        for (int o = 1; o < 4; o <<= 1) {
+            const float om = __shfl_xor_sync(kFull, mm, o), ol = __shfl_xor_sync(kFull, ll, o);
+            merge(mm, ll, om, ol);
+            if (ol != ol) ll = ol;
         }
+        if (t == 0) stat[warp][g + 8 * half] = make_float2(mm, ll);
+    }
     __syncthreads();
     for (int r = threadIdx.x; r < nr; r += blockDim.x) {
         float mm = -INFINITY, ll = 0.f;
         for (int x = 0; x < groups; ++x) {
-            const float2 y = stat[x * wr + r / (16 * MR)][r % (16 * MR)];
+            const float2 y = stat[x * wr + r / 16][r % 16];
             merge(mm, ll, y.x, y.y);
             if (y.y != y.y) ll = y.y;
         }
@@ -1116,7 +1103,7 @@ ManyPlan many_plan(int B, int H, int R, int C)
 
 bool g_many_attr[64][3];
 
-template <int NB, int MR>
+template <int NB>
 int launch_many(ScoreArgs a, int nb_index, cudaStream_t st)
 {
     int dev = 0;
@@ -1124,7 +1111,7 @@ int launch_many(ScoreArgs a, int nb_index, cudaStream_t st)
     {
         std::lock_guard<std::mutex> lock(g_score_mu);
         if (!g_many_attr[dev][nb_index]) {
-            if (cudaFuncSetAttribute(k_score_rows<NB, MR>, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024 - 4096) !=
+            if (cudaFuncSetAttribute(k_score_rows<NB>, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024 - 4096) !=
                     cudaSuccess ||
                 cudaFuncSetAttribute(k_score_slots<NB>, cudaFuncAttributeMaxDynamicSharedMemorySize, 128 * 1024) !=
                     cudaSuccess)
@@ -1136,7 +1123,7 @@ int launch_many(ScoreArgs a, int nb_index, cudaStream_t st)
     // warps beyond the rows' take slots of their own, as far as their stages
     // leave room for two blocks a SM: 64 slots each for one or two groups, 32
     // for more
-    const int wr = static_cast<int>(ceil_div(top, 16 * MR));
+    const int wr = static_cast<int>(ceil_div(top, 16));
     const int fit = static_cast<int>(kScoreSmem / (kRowStages * 32 / 8 * NB * 512));
     const int groups = std::max(1, std::min(kScoreWarps / wr, fit));
     const int row_slots = groups > fit / 2 ? 32 : 64;
@@ -1144,7 +1131,7 @@ int launch_many(ScoreArgs a, int nb_index, cudaStream_t st)
     const int slots = a.slots;
     a.slots = row_slots;
     const unsigned heads = static_cast<unsigned>(a.B * a.H);
-    k_score_rows<NB, MR><<<dim3(static_cast<unsigned>(a.chunks), static_cast<unsigned>(ceil_div(a.R, kManyRows)), heads),
+    k_score_rows<NB><<<dim3(static_cast<unsigned>(a.chunks), static_cast<unsigned>(ceil_div(a.R, kManyRows)), heads),
                            32 * wr * groups, ring, st>>>(a);
     if (cudaGetLastError() != cudaSuccess) return SPEC_ECUDA;
     a.slots = slots;
@@ -1275,9 +1262,9 @@ extern "C" int spec_cache_score(const void *q, const void *k, spec_dtype_t dtype
         a.chunks = many.chunks;
         a.slots = many.slots;
         a.minus_l = reinterpret_cast<float *>(static_cast<char *>(workspace) + many.stats_bytes);
-        if (head_dim <= 64) return launch_many<2, 2>(a, 0, stream);
-        if (head_dim <= 128) return launch_many<4, 2>(a, 1, stream);
-        return launch_many<8, 1>(a, 2, stream);
+        if (head_dim <= 64) return launch_many<2>(a, 0, stream);
+        if (head_dim <= 128) return launch_many<4>(a, 1, stream);
+        return launch_many<8>(a, 2, stream);
     }
     const ScorePlan plan = score_plan(batch, kv_heads, a.R, head_dim, capacity, f32);
     if (static_cast<int64_t>(batch) * kv_heads * plan.blocks > INT_MAX) return SPEC_EUNSUPPORTED;

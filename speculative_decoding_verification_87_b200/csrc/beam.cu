@@ -98,6 +98,18 @@ struct BeamRows {
     int exact[SPEC_MAX_BEAMS];    // 1: recompute wanted, 2: done
 };
 
+// This lane's vector v of item s of row w, -inf past the vocabulary.
+template <class Tag>
+__device__ __forceinline__ uint4 item_vector(const Params &p, int b, int w, int s, int v)
+{
+    constexpr int kVec = Tag::kVec;
+    constexpr int kEsz = sizeof(typename Tag::elem);
+    const int e = s * Pass1Shape<Tag>::kItem + (v * 32 + static_cast<int>(threadIdx.x & 31)) * kVec;
+    const char *row = static_cast<const char *>(p.tl) + (static_cast<int64_t>(b) * p.R + w) * p.stride * kEsz;
+    return e < p.V ? mask_tail<Tag>(ldg_vec(row + static_cast<int64_t>(e) * kEsz), p.V - e)
+                   : make_uint4(Tag::kNegInfWord, Tag::kNegInfWord, Tag::kNegInfWord, Tag::kNegInfWord);
+}
+
 // Append the candidates of one item (row w, segment s) that reach lthr to
 // the list.  One warp.  *count is the list's new length, which may pass cap
 // (entries beyond it are not stored).  A vector's packed maximum decides
@@ -114,11 +126,7 @@ __device__ __forceinline__ void gather_item(const Params &p, int b, int w, int s
     const int lane = threadIdx.x & 31;
     const int e0 = s * Pass1Shape<Tag>::kItem + lane * kVec;
     const char *row = static_cast<const char *>(p.tl) + (static_cast<int64_t>(b) * p.R + w) * p.stride * kEsz;
-    auto vector = [&](int v) -> uint4 {
-        const int e = e0 + v * 32 * kVec;
-        return e < p.V ? mask_tail<Tag>(ldg_vec(row + static_cast<int64_t>(e) * kEsz), p.V - e)
-                       : make_uint4(Tag::kNegInfWord, Tag::kNegInfWord, Tag::kNegInfWord, Tag::kNegInfWord);
-    };
+    auto vector = [&](int v) { return item_vector<Tag>(p, b, w, s, v); };
     auto reaches = [&](uint4 raw) {
         const float top = vec_max<Tag>(raw);
         return top >= lthr && top > -INFINITY;
@@ -266,16 +274,17 @@ __global__ void __launch_bounds__(kBeamThreads)
     const float2 *part = p.rowpart + static_cast<int64_t>(b) * W * S;
     const int items = W * S;
     const float inv_t = static_cast<float>(p.inv_t);
-    // score of the best candidate of item s of row w (-inf: none), in fp32
-    auto item_key = [&](int w, int s) -> float {
-        const int i = w * S + s;
-        const float m = i < kHeldItems ? held[i] : __ldcg(&part[i].x);
-        return rw.kind[w] != kRowLive || m == -INFINITY ? -INFINITY : fmaf(m - rw.m[w], inv_t, rw.base32[w]);
+    auto row_of = [&](int i) { return static_cast<int>(fdiv(static_cast<unsigned>(i), p.div_s)); };
+    // score of row w's logit l (-inf: no candidate), in fp32
+    auto key_of = [&](int w, float l) -> float {
+        return rw.kind[w] != kRowLive || l == -INFINITY ? -INFINITY : fmaf(l - rw.m[w], inv_t, rw.base32[w]);
     };
+    // score of the best candidate of item i (item s of row w: w S + s)
+    auto item_key = [&](int i) -> float { return key_of(row_of(i), i < kHeldItems ? held[i] : __ldcg(&part[i].x)); };
     // and in fp64
-    auto item_score = [&](int w, int s) -> double {
+    auto item_score = [&](int i) -> double {
+        const int w = row_of(i);
         if (rw.kind[w] != kRowLive) return -INFINITY;
-        const int i = w * S + s;
         const float m = i < kHeldItems ? held[i] : __ldcg(&part[i].x);
         return m == -INFINITY ? -INFINITY
                               : rw.base[w] + (static_cast<double>(m) - static_cast<double>(rw.m[w])) * p.inv_t;
@@ -349,8 +358,7 @@ __global__ void __launch_bounds__(kBeamThreads)
             // a lower bound t0 of the K-th best candidate: the K-th largest of
             // kGroups maxima of distinct items (each a candidate's score)
             float mine = -INFINITY;
-            for (int w = warp; w < W; w += kBeamWarps)
-                for (int i = lane; i < S; i += 32) mine = fmaxf(mine, item_key(w, i));
+            for (int i = tid; i < items; i += kBeamThreads) mine = fmaxf(mine, item_key(i));
             thread_max[tid] = mine;
             if (tid == 0) {
                 nlist = 0;
@@ -359,10 +367,10 @@ __global__ void __launch_bounds__(kBeamThreads)
                 bound = 0xFFFFFFFFu;
             }
             __syncthreads();
-            // groups of threads of different warps, so of different rows where
-            // rows are many: the best row's best items stay apart
+            // every kGroups-th item to a group: as many groups as items, up to
+            // kGroups, and the best row's best items in different ones
             if (tid < kGroups) {
-    #pragma unroll
+#pragma unroll
                 for (int x = kGroups; x < kBeamThreads; x += kGroups) mine = fmaxf(mine, thread_max[tid + x]);
                 group_max[tid] = mine;
             }
@@ -385,20 +393,41 @@ __global__ void __launch_bounds__(kBeamThreads)
                 if (lane == 0) atomicMin(&bound, least);
             }
             __syncthreads();
-            const float t0f = order_value(bound);
+            float t0f = order_value(bound);
+            if (t0f == -INFINITY && real) {
+                // fewer than K items: the K-th largest of the maxima of their
+                // parts, 32 bf16 (16 fp32) entries a lane and half
+                float sub[2] = {-INFINITY, -INFINITY};
+                for (int i = warp; i < items; i += kBeamWarps) {
+                    const int w = row_of(i);
+                    if (rw.kind[w] != kRowLive) continue;
+#pragma unroll 1
+                    for (int v = 0; v < Pass1Shape<Tag>::kVecL; ++v) {
+                        const float key = key_of(w, vec_max<Tag>(item_vector<Tag>(p, b, w, i - w * S, v)));
+                        if (v < Pass1Shape<Tag>::kVecL / 2) sub[0] = fmaxf(sub[0], key);
+                        else sub[1] = fmaxf(sub[1], key);
+                    }
+                }
+                const uint32_t k0 = order_key(sub[0]), k1 = order_key(sub[1]);
+                uint32_t lo = order_key(-INFINITY), hi = order_key(INFINITY);
+                while (lo < hi) {
+                    const uint32_t mid = lo + (hi - lo + 1) / 2;
+                    if (__syncthreads_count(k0 >= mid) + __syncthreads_count(k1 >= mid) >= K) lo = mid;
+                    else hi = mid - 1;
+                }
+                t0f = order_value(lo);
+            }
             // below t0 by the rows' errors, so that what the check below
             // compares is in the list too; and by the keys' rounding, at most
             // 4 steps of what adds up to a key
             const double t0 = t0f == -INFINITY ? -INFINITY : static_cast<double>(t0f) - 4.0 * kBaseErr;
             auto slack = [&](int w) { return 4.8e-7f * (fabsf(t0f) + fabsf(rw.base32[w])); };
-            for (int w = warp; w < W; w += kBeamWarps) {
-                const float least = t0f == -INFINITY ? -INFINITY : static_cast<float>(t0) - 2.f * slack(w);
-                for (int i = lane; i < S; i += 32) {
-                    const float key = item_key(w, i);
-                    if (key >= least && key > -INFINITY) {
-                        const int at = atomicAdd(&nlist, 1);
-                        if (at < kListMax) list[at] = w * S + i;
-                    }
+            const float least = t0f == -INFINITY ? -INFINITY : static_cast<float>(t0);
+            for (int i = tid; i < items; i += kBeamThreads) {
+                const float key = item_key(i);
+                if (key > -INFINITY && key >= least - 2.f * slack(row_of(i))) {
+                    const int at = atomicAdd(&nlist, 1);
+                    if (at < kListMax) list[at] = i;
                 }
             }
             auto add_done = [&]() {
@@ -410,7 +439,7 @@ __global__ void __launch_bounds__(kBeamThreads)
             bool whole = nlist <= kListMax;
             if (whole) {
                 for (int j = warp; j < (real ? nlist : min(nlist, kBeamWarps)); j += kBeamWarps) {
-                    const int w = list[j] / S;
+                    const int w = row_of(list[j]);
                     // the row's logits that may reach t0, rounded down
                     float lthr = -INFINITY;
                     if (t0 != -INFINITY) {
@@ -434,7 +463,8 @@ __global__ void __launch_bounds__(kBeamThreads)
                 for (; n < K; ++n) {
                     Cand top = {-INFINITY, INT_MAX, INT_MAX};
                     for (int i = tid; i < items; i += kBeamThreads) {
-                        const Cand c = {item_score(i / S, i % S), i / S, i % S};
+                        const int w = row_of(i);
+                        const Cand c = {item_score(i), w, i - w * S};
                         if (c.s > -INFINITY && better(last, c) && better(c, top)) top = c;
                     }
     #pragma unroll
@@ -455,7 +485,7 @@ __global__ void __launch_bounds__(kBeamThreads)
                 }
                 __syncthreads();
                 for (int j = warp; j < n; j += kBeamWarps) {
-                    const int w = list[j] / S;
+                    const int w = row_of(list[j]);
                     gather_best<Tag>(p, b, w, list[j] - w * S, rw.base[w], rw.m[w], K, cand, a.cap, &ncand);
                 }
                 if (tid == 0) nlist = n;
@@ -502,8 +532,8 @@ __global__ void __launch_bounds__(kBeamThreads)
                 // leaves out only what lies further below)
                 if (!whole && real)
                     for (int i = tid; i < items; i += kBeamThreads) {
-                        const int w = i / S;
-                        const double s = item_score(w, i % S);
+                        const int w = row_of(i);
+                        const double s = item_score(i);
                         if (s == -INFINITY || !close(kth, s, w)) continue;
                         bool in = false;
                         for (int j = 0; j < nlist && !in; ++j) in = list[j] == i;

@@ -89,6 +89,18 @@ def test_equal_candidates_go_to_the_lowest_index(sv, dtype, B, W, K, V):
     check(sv, x, torch.full((B, W), -2.5), V, K)
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("B, W, K, V", [(2, 1, 16, 2000), (3, 1, 64, 5000), (2, 3, 64, 1500), (20, 20, 10, 4006), (1, 2, 33, 1024),
+                                        (2, 1, 64, 70), (1, 1, 40, 32001)])
+def test_fewer_items_than_beams_kept(sv, dtype, B, W, K, V):
+    x, s = rows(V + K, B, W, V, dtype)
+    check(sv, x, s, V, K)
+    m = torch.rand(x.shape, generator=torch.Generator().manual_seed(2)) < 0.9
+    x[m] = -float("inf")
+    x[:, :, 0] = 0.0
+    check(sv, x, s, V, K, 0.6)
+
+
 def test_ties_inside_and_across_items(sv):
     # a few values only, so that the K-th best ties with many others
     g = torch.Generator().manual_seed(3)

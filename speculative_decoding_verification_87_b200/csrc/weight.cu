@@ -8,13 +8,11 @@
 // units of log2 (scale log2 e multiplies the products), sums and statistics
 // in fp32.
 //
-// One kernel: a cluster of blocks per (request, head), each with a slice of
-// the slots.  The products go to the block's shared memory, become
-// e = 2^(s - m) with the block's own row maxima m there, the blocks exchange
-// (m, sum e) per row through distributed shared memory, and slot t gains
-// sum_r e_rt 2^(m_r - L_r): the keys are read once and there is one
-// exponential per product.  A slice whose products do not fit is swept in
-// parts twice, once for the statistics and once for the weights.
+// Two forms.  Few rows (decoding): the keys are read once, their products
+// stored and added up by a second kernel.  Many rows (a prompt's last
+// queries): two sweeps over the keys that keep everything in registers.  Both
+// spread a head's slots over the whole GPU and merge the chunks' (max, sum)
+// per row in between.
 //
 // Products run on mma.sync m16n8k16 with 16 rows as A and 8 slots as B.  The
 // sum over d may run in any order, so a lane's 16 contiguous bytes (8
@@ -35,7 +33,6 @@
 #include <mutex>
 #include <type_traits>
 
-#include <cooperative_groups.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -45,33 +42,25 @@
 namespace sv {
 namespace {
 
-namespace cg = cooperative_groups;
-
 constexpr int kScoreThreads = 256;
 constexpr int kScoreWarps = kScoreThreads / 32;
-constexpr int kClusterMax = 16;
-constexpr int kPartSlots = 128;     // a swept part is a multiple of this: 16 slots a warp
+constexpr int kPartSlots = 128;     // the shortest chunk of slots: 16 a warp
 
 struct ScoreArgs {
     const void *q, *k;
     int64_t q_req, q_tok, q_head, k_req, k_head, k_slot;  // elements
     const int32_t *begin, *end;
     int B, Q, H, G, D, C;  // H key heads, C capacity
-    int blocks;            // of a cluster
-    int tile_rows;         // rows of a row tile (a multiple of 16)
-    int held_rows;         // of them, rows whose products are stored
-    int part;              // slots whose products fit shared memory
-    int pitch;             // words between rows of products
+    int R;                 // Q * G
+    int part, chunks;      // slots of a chunk of the statistics, chunks
     float scale2;          // scale * log2(e)
     const float *in;
     float *out;
     int32_t *status;
-    // few and many rows
-    int R;                 // Q * G
-    int chunks;            // chunks of `part` slots (statistics)
     int slots;             // slots of a block (weights), of a warp's stage (statistics)
     float2 *stats;         // [B][H][R][chunks]
     float *minus_l;        // many rows: -L [B][H][R]
+    int pitch;             // few rows: words between rows of products
     float *held;           // few rows: products [B][H][R][pitch]
 };
 
@@ -295,160 +284,6 @@ __device__ __forceinline__ void products(const Slots<Tag, NB> &k, const uint4 *s
     }
 }
 
-template <class Tag, int NB>
-__global__ void __launch_bounds__(kScoreThreads, 2) k_score(const __grid_constant__ ScoreArgs a)
-{
-    extern __shared__ __align__(16) unsigned char smem[];
-    cg::cluster_group cluster = cg::this_cluster();
-    const int rank = static_cast<int>(cluster.block_rank()), blocks = a.blocks;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int64_t head = blockIdx.x / blocks;
-    const int b = static_cast<int>(head / a.H), h = static_cast<int>(head % a.H);
-    const Span sp = span_of(a, b);
-    if (!sp.ok) {  // the whole cluster leaves
-        if (tid == 0 && rank == 0 && h == 0 && a.status) atomicOr(a.status, SPEC_STATUS_CAPACITY);
-        return;
-    }
-    const int nb = (a.D + 31) / 32;
-    // shared memory: query fragments, products, row statistics and factors
-    uint4 *sq = reinterpret_cast<uint4 *>(smem);
-    float *ss = reinterpret_cast<float *>(sq + a.tile_rows / 16 * nb * Parts<Tag>::kParts * 64);
-    float2 *stat = reinterpret_cast<float2 *>(ss + a.held_rows * a.pitch);  // [units]
-    float *fac = reinterpret_cast<float *>(stat + max(a.tile_rows, kScoreWarps));               // [units]
-
-    const int rows = (sp.end - sp.begin) * a.G;
-    const auto *keys = static_cast<const typename Tag::elem *>(a.k) + b * a.k_req + h * a.k_head;
-    const float *in = a.in + head * a.C;
-    float *out = a.out + head * a.C;
-    // the block's slots, whole m-tiles
-    const int slice = ((sp.end + blocks - 1) / blocks + 15) / 16 * 16;
-    const int s0 = min(sp.end, rank * slice), s1 = min(sp.end, s0 + slice);
-    const bool once = s1 - s0 <= a.part;
-
-    if (rows == 0) {
-        for (int t = s0 + tid; t < s1; t += kScoreThreads) out[t] = in[t];
-        return;
-    }
-    for (int r0 = 0; r0 < rows; r0 += a.tile_rows) {
-        const int nr = min(rows - r0, a.tile_rows), tiles = (nr + 15) / 16;
-        // a row's slots are shared by `split` warps where rows are few
-        const int split = nr <= 1 ? 8 : nr <= 2 ? 4 : nr <= 4 ? 2 : 1;
-        __syncthreads();
-        stage_rows<Tag>(a, b, h, r0, rows, tiles, nb, sq);
-        for (int i = tid; i < nr * split; i += kScoreThreads) stat[i] = make_float2(-INFINITY, 0.f);
-        __syncthreads();
-
-        // products of slots [p0, p1) into ss[row][slot - p0], -inf where unseen
-        auto fill = [&](int p0, int p1) {
-            Slots<Tag, NB> cur, next;
-            int t0 = p0 + warp * 16;
-            if (t0 < p1) cur.load(a, keys, t0, p1);
-            for (; t0 < p1; t0 += kScoreWarps * 16) {
-                if (t0 + kScoreWarps * 16 < p1) next.load(a, keys, t0 + kScoreWarps * 16, p1);
-                const int g = lane >> 2, t2 = 2 * (lane & 3);
-                for (int tile0 = 0; tile0 < tiles; ++tile0) {
-                    float c[1][2][4];
-                    products<Tag, NB, 1>(cur, sq, nb, tile0, tiles, c);
-#pragma unroll
-                    for (int half = 0; half < 2; ++half)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const int r = tile0 * 16 + g + 8 * (e >> 1), t = t0 + 8 * half + t2 + (e & 1);
-                            if (r < nr) {
-                                const bool seen = t < p1 && (t <= sp.begin || t <= sp.begin + (r0 + r) / a.G);
-                                ss[r * a.pitch + t - p0] = seen ? c[0][half][e] * a.scale2 : -INFINITY;
-                            }
-                        }
-                }
-                cur = next;
-            }
-        };
-        // row statistics of the part, merged into stat; with `keep` the
-        // products become 2^(s - m)
-        auto statistics = [&](int n, bool keep) {
-            const int span = ((n + split - 1) / split + 31) / 32 * 32;
-            for (int u = warp; u < nr * split; u += kScoreWarps) {
-                float *row = ss + (u / split) * a.pitch;
-                const int i0 = min(n, (u % split) * span), i1 = min(n, i0 + span);
-                float m = -INFINITY;
-                for (int i = i0 + lane; i < i1; i += 32) m = max_nan(m, row[i]);
-                m = warp_max_nan(m);
-                float l = 0.f;
-                if (m != -INFINITY || keep)
-                    for (int i = i0 + lane; i < i1; i += 32) {
-                        const float e = m == -INFINITY ? 0.f : ex2_approx(row[i] - m);
-                        l += e;
-                        if (keep) row[i] = e;
-                    }
-                l = warp_sum(l);
-                if (lane == 0) {
-                    float2 x = stat[u];
-                    merge(x.x, x.y, m, l);
-                    stat[u] = x;
-                }
-            }
-        };
-        // slots [p0, p1): the weights of this row tile, from 2^(s - m) and
-        // factors, or from the products and L
-        auto apply = [&](int p0, int p1, bool kept) {
-            const int n = p1 - p0;
-            const int span = ((n + split - 1) / split + 31) / 32 * 32;
-            for (int i = tid; i < n; i += kScoreThreads) {
-                const int t = p0 + i;
-                const float *col = ss + i;
-                float sum = 0.f;
-                if (t <= sp.begin) {  // seen by every row
-                    if (kept) {
-                        const float *f = fac + i / span;
-                        for (int r = 0; r < nr; ++r) sum = fmaf(col[r * a.pitch], f[r * split], sum);
-                    } else {
-                        for (int r = 0; r < nr; ++r) sum += ex2_approx(col[r * a.pitch] - fac[r]);
-                    }
-                } else {
-                    const int first = max(0, (t - sp.begin) * a.G - r0);
-                    for (int r = first; r < nr; ++r)
-                        sum += kept ? col[r * a.pitch] * fac[r * split + i / span] : ex2_approx(col[r * a.pitch] - fac[r]);
-                }
-                const float old = r0 > 0 ? out[t] : t < sp.begin ? in[t] : 0.f;
-                out[t] = old + sum;
-            }
-        };
-
-        for (int p0 = s0; p0 < s1; p0 += a.part) {
-            const int p1 = min(s1, p0 + a.part);
-            fill(p0, p1);
-            __syncthreads();
-            statistics(p1 - p0, once);
-            __syncthreads();
-        }
-        // L of every row, from all blocks and splits in a fixed order
-        cluster.sync();
-        for (int r = tid; r < nr; r += kScoreThreads) {
-            float m = -INFINITY, l = 0.f;
-            for (int k = 0; k < blocks; ++k) {
-                const float2 *other = cluster.map_shared_rank(stat, k);
-                for (int x = 0; x < split; ++x) {
-                    const float2 y = other[r * split + x];
-                    merge(m, l, y.x, y.y);
-                }
-            }
-            const float L = m + log2f(l);
-            for (int x = 0; x < split; ++x)
-                fac[once ? r * split + x : r] = once ? ex2_approx(stat[r * split + x].x - L) : L;
-        }
-        cluster.sync();  // stat is read everywhere; fac is complete here
-        for (int p0 = s0; p0 < s1; p0 += a.part) {
-            const int p1 = min(s1, p0 + a.part);
-            if (!once) {
-                fill(p0, p1);
-                __syncthreads();
-            }
-            apply(p0, p1, once);
-            __syncthreads();
-        }
-    }
-}
-
 // ------------------------------------------------------------------ few rows
 // Decoding and small verifications: reading the keys bounds the step, so they
 // are read once.  k_score_few forms the products, stores them and the
@@ -622,12 +457,10 @@ __global__ void __launch_bounds__(kScoreThreads) k_score_sum(const __grid_consta
         if (t + i < sp.end) out[t + i] = sum[i] + w[i];
 }
 
-// --------------------------------------------------------- many rows (bf16)
+// ------------------------------------------------------------------ many rows
 // Where a key head has many rows (a prompt's last queries, a verification with
 // wide groups) the products no longer fit shared memory and the exponentials
-// and the tensor pipe bound the step, not the keys.  Two sweeps, no cluster
-// (16 blocks of one SM each fit only some of the processing clusters, and
-// eight would leave SMs idle):
+// and the tensor pipe bound the step, not the keys.  Two sweeps:
 //   k_score_rows   a warp holds 16 rows as A fragments in registers, the keys
 //                  stream through shared memory as B fragments for all warps; the
 //                  running (max, sum) of a row stays in its four lanes (its
@@ -639,66 +472,109 @@ __global__ void __launch_bounds__(kScoreThreads) k_score_sum(const __grid_consta
 // halve its time, but drop what falls below the running sum at each of the
 // D / 16 steps, and the weights came out 6e-6 off (2-norm, against 3e-7 here)
 // on peaked keys; mma.sync keeps fp32 accuracy.
-constexpr int kManyRows = 128;     // rows of a row tile
+// Rows of a row tile, tiles of 8 slots a warp of the weights sweep and blocks a
+// SM: fp32 rows take three times a bf16 row's shared memory and fp32 slots
+// twice the registers.
+template <class Tag>
+struct Many;
+template <>
+struct Many<Bf16> {
+    static constexpr int kRows = 128, kBlocks = 2;
+    template <int NB>
+    static constexpr int kTiles = NB <= 4 ? 4 : 2;
+};
+template <>
+struct Many<F32> {
+    static constexpr int kRows = 64, kBlocks = 1;
+    template <int NB>
+    static constexpr int kTiles = NB <= 2 ? 4 : NB <= 4 ? 2 : 1;
+};
 constexpr int kRowStages = 3;
 
-// Slots [t0, t0 + slots) below `end` as B fragments (512 bytes per 8 slots
-// and 32 elements, NB * 32 elements a slot), asynchronously; the rest as
-// zeros.
-template <int NB>
-__device__ __forceinline__ void copy_slots(const ScoreArgs &a, const uint16_t *keys, int t0, int slots, int end, uint4 *dst)
+// Slots [t0, t0 + slots) below `end` as B fragments (512 bytes per 8 slots and
+// 32 elements, 1024 for fp32: a lane's first and second 16 bytes apart),
+// NB * 32 elements a slot, asynchronously; the rest as zeros.
+template <class Tag, int NB>
+__device__ __forceinline__ void copy_slots(const ScoreArgs &a, const typename Tag::elem *keys, int t0, int slots, int end,
+                                           uint4 *dst)
 {
-    constexpr int kChunks = 4 * NB;
+    constexpr int kRaw = Parts<Tag>::kRaw, kChunks = 4 * NB * kRaw;
     for (int i = threadIdx.x; i < slots * kChunks; i += blockDim.x) {
         const int slot = i / kChunks, c = i % kChunks;
-        const bool in = t0 + slot < end && c * 8 < a.D;
-        const uint16_t *from = in ? keys + (t0 + slot) * a.k_slot + c * 8 : keys;
-        const uint32_t at = static_cast<uint32_t>(
-            __cvta_generic_to_shared(dst + ((slot >> 3) * NB + (c >> 2)) * 32 + (slot & 7) * 4 + (c & 3)));
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(at), "l"(from), "r"(in ? 16 : 0) : "memory");
+        const bool in = t0 + slot < end && c * Tag::kVec < a.D;
+        const auto *from = in ? keys + (t0 + slot) * a.k_slot + c * Tag::kVec : keys;
+        uint4 *to = dst + ((slot >> 3) * NB + c / (4 * kRaw)) * 32 * kRaw + c % kRaw * 32 + (slot & 7) * 4 + c / kRaw % 4;
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(
+                         static_cast<uint32_t>(__cvta_generic_to_shared(to))),
+                     "l"(from), "r"(in ? 16 : 0)
+                     : "memory");
     }
+}
+
+// c += the products of a row tile's parts (two k-steps lo, hi) with 8 slots'
+// parts, the smaller ones first; FIRST: c = for bf16.
+template <class Tag, bool FIRST>
+__device__ __forceinline__ void tile_products(float (&c)[4], const uint4 (&lo)[Parts<Tag>::kParts],
+                                              const uint4 (&hi)[Parts<Tag>::kParts], const uint4 (&w)[Parts<Tag>::kParts])
+{
+    constexpr int kP = Parts<Tag>::kParts;
+    if (FIRST && kP > 1) c[0] = c[1] = c[2] = c[3] = 0.f;
+#pragma unroll
+    for (int s = kP - 1; s >= 0; --s)
+#pragma unroll
+        for (int x = s; x >= 0; --x) {
+            const uint4 u = lo[x], v = hi[x], y = w[s - x];
+            if (FIRST && kP == 1) mma_bf16_first(c, u.x, u.y, u.z, u.w, y.x, y.y);
+            else mma_bf16(c, u.x, u.y, u.z, u.w, y.x, y.y);
+            mma_bf16(c, v.x, v.y, v.z, v.w, y.z, y.w);
+        }
 }
 
 // Statistics of the rows of one tile over one chunk of slots: grid (chunk,
 // row tile, request and head).
-template <int NB>
-__global__ void __launch_bounds__(kScoreThreads, 2) k_score_rows(const __grid_constant__ ScoreArgs a)
+template <class Tag, int NB>
+__global__ void __launch_bounds__(kScoreThreads, Many<Tag>::kBlocks) k_score_rows(const __grid_constant__ ScoreArgs a)
 {
+    constexpr int kP = Parts<Tag>::kParts, kRaw = Parts<Tag>::kRaw, kRows = Many<Tag>::kRows;
     extern __shared__ __align__(16) unsigned char smem[];
     uint4 *ring = reinterpret_cast<uint4 *>(smem);
     __shared__ float2 stat[kScoreWarps][16];
     const int64_t head = blockIdx.z;
     const int b = static_cast<int>(head / a.H), h = static_cast<int>(head % a.H);
     const Span sp = span_of(a, b);
-    const int rows = (sp.end - sp.begin) * a.G, r0 = blockIdx.y * kManyRows;
+    const int rows = (sp.end - sp.begin) * a.G, r0 = blockIdx.y * kRows;
     const int t_begin = blockIdx.x * a.part, t_end = min(sp.end, t_begin + a.part);
     asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
     if (!sp.ok || r0 >= rows || t_begin >= t_end) return;
-    const int nr = min(rows - r0, kManyRows);
+    const int nr = min(rows - r0, kRows);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
-    const int wr = (min(a.R, kManyRows) + 15) / 16;  // warps over the rows
-    const int groups = (blockDim.x >> 5) / wr;                          // groups of them over the slots
-    const int row_slots = a.slots;                                      // of a stage, for each group
+    const int wr = (min(a.R, kRows) + 15) / 16;  // warps over the rows
+    const int groups = (blockDim.x >> 5) / wr;   // groups of them over the slots
+    const int row_slots = a.slots;               // of a stage, for each group
     const int rw = (warp % wr) * 16, sg = warp / wr;
-    const auto *keys = static_cast<const uint16_t *>(a.k) + b * a.k_req + h * a.k_head;
-    const int stage_slots = row_slots * groups, stage = stage_slots / 8 * NB * 32;  // uint4
+    const auto *keys = static_cast<const typename Tag::elem *>(a.k) + b * a.k_req + h * a.k_head;
+    const int stage_slots = row_slots * groups, stage = stage_slots / 8 * NB * 32 * kRaw;  // uint4
     const int stages = (t_end - t_begin + stage_slots - 1) / stage_slots;
-    // this warp's rows, by way of the ring: lane (g, t) holds rows g and g + 8
-    // of each 16
-    stage_rows<Bf16>(a, b, h, r0, rows, (nr + 15) / 16, NB, ring);
+    // This warp's rows: lane (g, t) holds rows g and g + 8.  bf16: in
+    // registers, by way of the ring; fp32: read from behind the ring.
+    uint4 *sq = kP == 1 ? ring : ring + kRowStages * stage;
+    stage_rows<Tag>(a, b, h, r0, rows, (nr + 15) / 16, NB, sq);
     __syncthreads();
-    uint4 q[NB][2];
+    const uint4 *own = sq + rw / 16 * NB * kP * 64 + lane;  // (j * kP + part) * 64 + 32 * k-step
+    uint4 q[kP == 1 ? NB : 1][2];
     int last[2];  // the last slot a row sees
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
         last[half] = sp.begin + (r0 + rw + g + 8 * half) / a.G;
+        if (kP == 1) {
 #pragma unroll
-        for (int j = 0; j < NB; ++j)
-            q[j][half] = rw < nr ? ring[(rw / 16 * NB + j) * 64 + half * 32 + lane] : make_uint4(0u, 0u, 0u, 0u);
+            for (int j = 0; j < NB; ++j)
+                q[kP == 1 ? j : 0][half] = rw < nr ? own[j * 64 + half * 32] : make_uint4(0u, 0u, 0u, 0u);
+        }
     }
-    __syncthreads();
+    if (kP == 1) __syncthreads();
     for (int s = 0; s < kRowStages - 1; ++s) {
-        if (s < stages) copy_slots<NB>(a, keys, t_begin + s * stage_slots, stage_slots, t_end, ring + s * stage);
+        if (s < stages) copy_slots<Tag, NB>(a, keys, t_begin + s * stage_slots, stage_slots, t_end, ring + s * stage);
         asm volatile("cp.async.commit_group;\n" ::: "memory");
     }
     float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};  // of this lane's columns, m in units of log2
@@ -708,15 +584,23 @@ __global__ void __launch_bounds__(kScoreThreads, 2) k_score_rows(const __grid_co
     auto step = [&](const uint4 *tile, int t0, auto whole) {
         float c[4][4];
 #pragma unroll
-        for (int j = 0; j < NB; ++j)
+        for (int j = 0; j < NB; ++j) {
+            uint4 u[kP], v[kP];
+#pragma unroll
+            for (int x = 0; x < kP; ++x) {
+                u[x] = kP == 1 ? q[kP == 1 ? j : 0][0] : own[(j * kP + x) * 64];
+                v[x] = kP == 1 ? q[kP == 1 ? j : 0][1] : own[(j * kP + x) * 64 + 32];
+            }
 #pragma unroll
             for (int n = 0; n < 4; ++n) {
-                const uint4 w = tile[(n * NB + j) * 32];
-                const uint4 u = q[j][0], v = q[j][1];
-                if (j == 0) mma_bf16_first(c[n], u.x, u.y, u.z, u.w, w.x, w.y);
-                else mma_bf16(c[n], u.x, u.y, u.z, u.w, w.x, w.y);
-                mma_bf16(c[n], v.x, v.y, v.z, v.w, w.z, w.w);
+                uint4 raw[kRaw], w[kP];
+#pragma unroll
+                for (int x = 0; x < kRaw; ++x) raw[x] = tile[((n * NB + j) * kRaw + x) * 32];
+                Parts<Tag>::split(raw, w);
+                if (j == 0) tile_products<Tag, true>(c[n], u, v, w);
+                else tile_products<Tag, false>(c[n], u, v, w);
             }
+        }
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
             // the scaled products are rounded here and in k_score_slots
@@ -755,18 +639,18 @@ __global__ void __launch_bounds__(kScoreThreads, 2) k_score_rows(const __grid_co
         {
             const int next = s + kRowStages - 1;
             if (next < stages)
-                copy_slots<NB>(a, keys, t_begin + next * stage_slots, stage_slots, t_end, ring + next % kRowStages * stage);
+                copy_slots<Tag, NB>(a, keys, t_begin + next * stage_slots, stage_slots, t_end, ring + next % kRowStages * stage);
             asm volatile("cp.async.commit_group;\n" ::: "memory");
         }
         const int t0 = t_begin + s * stage_slots + sg * row_slots;
-        const uint4 *tile = ring + s % kRowStages * stage + sg * (row_slots / 8) * NB * 32 + lane;
+        const uint4 *tile = ring + s % kRowStages * stage + sg * (row_slots / 8) * NB * 32 * kRaw + lane;
         if (rw >= nr || t0 >= t_end) continue;
         if (t0 + row_slots <= min(t_end, sp.begin + 1)) {
 #pragma unroll 1
-            for (int n0 = 0; n0 < row_slots; n0 += 32) step(tile + n0 / 8 * NB * 32, t0 + n0, std::true_type{});
+            for (int n0 = 0; n0 < row_slots; n0 += 32) step(tile + n0 / 8 * NB * 32 * kRaw, t0 + n0, std::true_type{});
         } else {
 #pragma unroll 1
-            for (int n0 = 0; n0 < row_slots; n0 += 32) step(tile + n0 / 8 * NB * 32, t0 + n0, std::false_type{});
+            for (int n0 = 0; n0 < row_slots; n0 += 32) step(tile + n0 / 8 * NB * 32 * kRaw, t0 + n0, std::false_type{});
         }
     }
     asm volatile("cp.async.wait_group 0;\n" ::: "memory");
@@ -821,13 +705,14 @@ __global__ void __launch_bounds__(kScoreThreads) k_score_merge(const __grid_cons
 }
 
 // The weights of one chunk of slots: grid (chunk, request and head).
-template <int NB>
-__global__ void __launch_bounds__(kScoreThreads, 2) k_score_slots(const __grid_constant__ ScoreArgs a)
+template <class Tag, int NB>
+__global__ void __launch_bounds__(kScoreThreads, Many<Tag>::kBlocks) k_score_slots(const __grid_constant__ ScoreArgs a)
 {
-    constexpr int kN = NB <= 4 ? 4 : 2;  // tiles of 8 slots a warp
+    constexpr int kP = Parts<Tag>::kParts, kRaw = Parts<Tag>::kRaw, kRows = Many<Tag>::kRows;
+    constexpr int kN = Many<Tag>::template kTiles<NB>;  // tiles of 8 slots a warp
     extern __shared__ __align__(16) unsigned char smem[];
     uint4 *sq = reinterpret_cast<uint4 *>(smem);
-    __shared__ __align__(8) float minus_l[kManyRows];
+    __shared__ float minus_l[kRows];
     const int64_t head = blockIdx.y;
     const int b = static_cast<int>(head / a.H), h = static_cast<int>(head % a.H);
     const Span sp = span_of(a, b);
@@ -839,31 +724,27 @@ __global__ void __launch_bounds__(kScoreThreads, 2) k_score_slots(const __grid_c
     const int t_begin = blockIdx.x * a.slots, t_end = min(sp.end, t_begin + a.slots);
     if (t_begin >= t_end) return;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
-    const auto *keys = static_cast<const uint16_t *>(a.k) + b * a.k_req + h * a.k_head;
+    const auto *keys = static_cast<const typename Tag::elem *>(a.k) + b * a.k_req + h * a.k_head;
     const float *in = a.in + head * a.C;
     float *out = a.out + head * a.C;
     const float sc = a.scale2;
-    for (int r0 = 0; r0 < max(rows, 1); r0 += kManyRows) {
-        const int nr = min(rows - r0, kManyRows), tiles = (nr + 15) / 16;
+    for (int r0 = 0; r0 < max(rows, 1); r0 += kRows) {
+        const int nr = min(rows - r0, kRows), tiles = (nr + 15) / 16;
         __syncthreads();
-        stage_rows<Bf16>(a, b, h, r0, rows, tiles, NB, sq);
+        stage_rows<Tag>(a, b, h, r0, rows, tiles, NB, sq);
         if (r0 == 0) asm volatile("griddepcontrol.wait;\n" ::: "memory");
         // a row that is none weighs nothing
         for (int r = threadIdx.x; r < tiles * 16; r += kScoreThreads)
             minus_l[r] = r < nr ? __ldcg(a.minus_l + head * a.R + r0 + r) : -INFINITY;
         __syncthreads();
         for (int t0 = t_begin + warp * 8 * kN; t0 < t_end; t0 += kScoreWarps * 8 * kN) {
-            uint4 k[kN][NB];  // lane (g, t): elements 32 j + 8 t .. + 7 of slot g of each 8
+            uint4 k[kN][NB][kRaw];  // lane (g, t): elements 32 j + 8 t .. + 7 of slot g of each 8
 #pragma unroll
             for (int n = 0; n < kN; ++n) {
                 const int slot = t0 + 8 * n + g;
                 const auto *row = keys + slot * a.k_slot;
 #pragma unroll
-                for (int j = 0; j < NB; ++j) {
-                    uint4 raw[1];
-                    load8<Bf16>(row, slot < t_end ? 32 * j + 8 * t : a.D, a.D, raw);
-                    k[n][j] = raw[0];
-                }
+                for (int j = 0; j < NB; ++j) load8<Tag>(row, slot < t_end ? 32 * j + 8 * t : a.D, a.D, k[n][j]);
             }
             // lane (g, t) writes slots 2 t, 2 t + 1 of tile g
             const int mine = t0 + 8 * g + 2 * t;
@@ -879,14 +760,19 @@ __global__ void __launch_bounds__(kScoreThreads, 2) k_score_slots(const __grid_c
                 float c[kN][4];
 #pragma unroll
                 for (int j = 0; j < NB; ++j) {
-                    const uint4 u = sq[(x * NB + j) * 64 + lane], v = sq[(x * NB + j) * 64 + 32 + lane];
+                    uint4 u[kP], v[kP];
 #pragma unroll
-                    for (int n = 0; n < kN; ++n) {
-                        if (j == 0) mma_bf16_first(c[n], u.x, u.y, u.z, u.w, k[n][j].x, k[n][j].y);
-                        else mma_bf16(c[n], u.x, u.y, u.z, u.w, k[n][j].x, k[n][j].y);
+                    for (int y = 0; y < kP; ++y) {
+                        u[y] = sq[((x * NB + j) * kP + y) * 64 + lane];
+                        v[y] = sq[((x * NB + j) * kP + y) * 64 + 32 + lane];
                     }
 #pragma unroll
-                    for (int n = 0; n < kN; ++n) mma_bf16(c[n], v.x, v.y, v.z, v.w, k[n][j].z, k[n][j].w);
+                    for (int n = 0; n < kN; ++n) {
+                        uint4 w[kP];
+                        Parts<Tag>::split(k[n][j], w);
+                        if (j == 0) tile_products<Tag, true>(c[n], u, v, w);
+                        else tile_products<Tag, false>(c[n], u, v, w);
+                    }
                 }
 #pragma unroll
                 for (int low = 0; low < 2; ++low) {
@@ -939,75 +825,7 @@ constexpr size_t kScoreAlign = 256;
 int64_t ceil_div(int64_t x, int64_t y) { return (x + y - 1) / y; }
 size_t align_up(size_t x) { return (x + kScoreAlign - 1) / kScoreAlign * kScoreAlign; }
 
-// How a call is laid out: blocks of a cluster, rows of a row tile, slots whose
-// products fit.  Two blocks share an SM (110 KB each).
-constexpr size_t kScoreSmem = 110 * 1024;
-struct ScorePlan {
-    int blocks, tile_rows, held_rows, part, pitch;
-    size_t smem;
-};
-ScorePlan score_plan(int B, int H, int R, int D, int C, bool f32)
-{
-    ScorePlan p;
-    // rows of a tile: their fragments, statistics and at least kPartSlots products
-    const int64_t row_bytes = ceil_div(D, 32) * 64 * (f32 ? 3 : 1) + 4 * (kPartSlots + 36) + 12;
-    const int64_t most = std::min<int64_t>(128, (kScoreSmem - 96) / row_bytes / 16 * 16);
-    const int64_t tiles = ceil_div(R, most);
-    p.tile_rows = static_cast<int>(ceil_div(ceil_div(R, tiles), 16) * 16);
-    p.held_rows = std::min(R, p.tile_rows);
-    const size_t frag = static_cast<size_t>(p.tile_rows) * ceil_div(D, 32) * 64 * (f32 ? 3 : 1);
-    const size_t stat = static_cast<size_t>(std::max(p.tile_rows, kScoreWarps)) * 12;
-    const int64_t words = static_cast<int64_t>((kScoreSmem - frag - stat) / 4 / static_cast<size_t>(p.held_rows));
-    // enough blocks for two on every SM, and so many that the slices fit
-    p.blocks = 1;
-    while (p.blocks < kClusterMax && p.blocks * kPartSlots < C &&
-           (static_cast<int64_t>(B) * H * p.blocks < 2 * 148 || ceil_div(C, p.blocks) + 36 > words))
-        p.blocks *= 2;
-    const int64_t slice = ceil_div(ceil_div(C, p.blocks), 16) * 16;
-    p.part = static_cast<int>(slice + 36 <= words ? slice : (words - 36) / kPartSlots * kPartSlots);
-    p.pitch = static_cast<int>(ceil_div(p.part, 32) * 32 + 4);
-    p.smem = frag + stat + sizeof(float) * static_cast<size_t>(p.pitch) * p.held_rows;
-    return p;
-}
-
 std::mutex g_score_mu;
-bool g_score_attr[64][2][3];
-
-template <class Tag, int NB>
-int launch_score(const ScoreArgs &a, size_t smem, int dtype_index, int nb_index, cudaStream_t st)
-{
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return SPEC_ECUDA;
-    {
-        std::lock_guard<std::mutex> lock(g_score_mu);
-        if (!g_score_attr[dev][dtype_index][nb_index]) {
-            if (cudaFuncSetAttribute(k_score<Tag, NB>, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024) !=
-                    cudaSuccess ||
-                cudaFuncSetAttribute(k_score<Tag, NB>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) !=
-                    cudaSuccess)
-                return SPEC_ECUDA;
-            g_score_attr[dev][dtype_index][nb_index] = true;
-        }
-    }
-    cudaLaunchConfig_t cfg = {};
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = static_cast<unsigned>(a.blocks);
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
-    cfg.gridDim = dim3(static_cast<unsigned>(static_cast<int64_t>(a.B) * a.H * a.blocks));
-    cfg.blockDim = dim3(kScoreThreads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = st;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    if (cudaLaunchKernelEx(&cfg, k_score<Tag, NB>, a) != cudaSuccess) {
-        (void)cudaGetLastError();
-        return SPEC_ECUDA;
-    }
-    return SPEC_OK;
-}
-
 // Few rows: while storing the products (8 bytes each, there and back) moves
 // less than a second read of the keys.
 bool few_rows(bool f32, int R, int D) { return R <= kFewRows && 8 * R < D * (f32 ? 4 : 2); }
@@ -1087,52 +905,61 @@ struct ManyPlan {
     int part, chunks, slots;
     size_t stats_bytes, l_bytes;
 };
+template <class Tag>
 ManyPlan many_plan(int B, int H, int R, int C)
 {
+    constexpr int64_t kWave = Many<Tag>::kBlocks * 148;
     ManyPlan p;
-    const int64_t heads = static_cast<int64_t>(B) * H, tiles = ceil_div(R, kManyRows);
-    const int64_t want = std::max<int64_t>(1, 2 * 148 / (heads * tiles));
+    const int64_t heads = static_cast<int64_t>(B) * H, tiles = ceil_div(R, Many<Tag>::kRows);
+    const int64_t want = std::max<int64_t>(1, kWave / (heads * tiles));
     p.part = static_cast<int>(ceil_div(ceil_div(C, want), 128) * 128);
     p.chunks = static_cast<int>(ceil_div(C, p.part));
-    const int64_t blocks = std::max<int64_t>(1, 2 * 148 / heads);
+    const int64_t blocks = std::max<int64_t>(1, kWave / heads);
     p.slots = static_cast<int>(ceil_div(ceil_div(C, blocks), 256) * 256);
     p.stats_bytes = align_up(sizeof(float2) * static_cast<size_t>(heads) * R * p.chunks);
     p.l_bytes = align_up(sizeof(float) * static_cast<size_t>(heads) * R);
     return p;
 }
 
-bool g_many_attr[64][3];
+bool g_many_attr[64][2][3];
 
-template <int NB>
-int launch_many(ScoreArgs a, int nb_index, cudaStream_t st)
+template <class Tag, int NB>
+int launch_many(ScoreArgs a, int dtype_index, int nb_index, cudaStream_t st)
 {
+    constexpr int kRows = Many<Tag>::kRows;
+    constexpr size_t kFrag = static_cast<size_t>(NB) * 1024 * Parts<Tag>::kParts;  // of 16 rows
+    constexpr size_t kSlotBytes = static_cast<size_t>(NB) * 64 * Parts<Tag>::kRaw;
+    // bf16: two blocks a SM, the rows in registers; fp32: one, the rows behind
+    // the ring
+    constexpr size_t kRing = Parts<Tag>::kParts == 1 ? 110 * 1024 : 220 * 1024 - kRows / 16 * kFrag;
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return SPEC_ECUDA;
     {
         std::lock_guard<std::mutex> lock(g_score_mu);
-        if (!g_many_attr[dev][nb_index]) {
-            if (cudaFuncSetAttribute(k_score_rows<NB>, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024 - 4096) !=
+        if (!g_many_attr[dev][dtype_index][nb_index]) {
+            if (cudaFuncSetAttribute(k_score_rows<Tag, NB>, cudaFuncAttributeMaxDynamicSharedMemorySize, 220 * 1024) !=
                     cudaSuccess ||
-                cudaFuncSetAttribute(k_score_slots<NB>, cudaFuncAttributeMaxDynamicSharedMemorySize, 128 * 1024) !=
-                    cudaSuccess)
+                cudaFuncSetAttribute(k_score_slots<Tag, NB>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                     static_cast<int>(kRows / 16 * kFrag)) != cudaSuccess)
                 return SPEC_ECUDA;
-            g_many_attr[dev][nb_index] = true;
+            g_many_attr[dev][dtype_index][nb_index] = true;
         }
     }
-    const int top = std::min(a.R, kManyRows);
-    // warps beyond the rows' take slots of their own, as far as their stages
-    // leave room for two blocks a SM: 64 slots each for one or two groups, 32
-    // for more
+    const int top = std::min(a.R, kRows);
+    // warps beyond the rows' take slots of their own, as far as the ring has
+    // room: 64 slots a stage each while it fits, else 32
     const int wr = static_cast<int>(ceil_div(top, 16));
-    const int fit = static_cast<int>(kScoreSmem / (kRowStages * 32 / 8 * NB * 512));
+    const int fit = static_cast<int>(kRing / (kRowStages * 32 * kSlotBytes));
+    static_assert(kRing >= kRowStages * 32 * kSlotBytes, "one group fits");
     const int groups = std::max(1, std::min(kScoreWarps / wr, fit));
     const int row_slots = groups > fit / 2 ? 32 : 64;
-    const size_t ring = static_cast<size_t>(kRowStages) * row_slots / 8 * groups * NB * 512;
+    const size_t ring = static_cast<size_t>(kRowStages) * row_slots * groups * kSlotBytes +
+                        (Parts<Tag>::kParts == 1 ? 0 : ceil_div(top, 16) * kFrag);
     const int slots = a.slots;
     a.slots = row_slots;
     const unsigned heads = static_cast<unsigned>(a.B * a.H);
-    k_score_rows<NB><<<dim3(static_cast<unsigned>(a.chunks), static_cast<unsigned>(ceil_div(a.R, kManyRows)), heads),
-                           32 * wr * groups, ring, st>>>(a);
+    k_score_rows<Tag, NB><<<dim3(static_cast<unsigned>(a.chunks), static_cast<unsigned>(ceil_div(a.R, kRows)), heads),
+                            32 * wr * groups, ring, st>>>(a);
     if (cudaGetLastError() != cudaSuccess) return SPEC_ECUDA;
     a.slots = slots;
     cudaLaunchConfig_t cfg = {};
@@ -1150,11 +977,11 @@ int launch_many(ScoreArgs a, int nb_index, cudaStream_t st)
     }
     cfg.gridDim = dim3(static_cast<unsigned>(ceil_div(a.C, a.slots)), heads);
     cfg.blockDim = dim3(kScoreThreads);
-    cfg.dynamicSmemBytes = ceil_div(top, 16) * NB * 1024;
+    cfg.dynamicSmemBytes = ceil_div(top, 16) * kFrag;
     cfg.stream = st;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    if (cudaLaunchKernelEx(&cfg, k_score_slots<NB>, a) != cudaSuccess) {
+    if (cudaLaunchKernelEx(&cfg, k_score_slots<Tag, NB>, a) != cudaSuccess) {
         (void)cudaGetLastError();
         return SPEC_ECUDA;
     }
@@ -1162,11 +989,16 @@ int launch_many(ScoreArgs a, int nb_index, cudaStream_t st)
 }
 
 template <class Tag>
-int launch_score(const ScoreArgs &a, size_t smem, int dtype_index, cudaStream_t st)
+int launch_many(ScoreArgs a, void *workspace, int dtype_index, cudaStream_t st)
 {
-    if (a.D <= 64) return launch_score<Tag, 2>(a, smem, dtype_index, 0, st);
-    if (a.D <= 128) return launch_score<Tag, 4>(a, smem, dtype_index, 1, st);
-    return launch_score<Tag, 8>(a, smem, dtype_index, 2, st);
+    const ManyPlan p = many_plan<Tag>(a.B, a.H, a.R, a.C);
+    a.part = p.part;
+    a.chunks = p.chunks;
+    a.slots = p.slots;
+    a.minus_l = reinterpret_cast<float *>(static_cast<char *>(workspace) + p.stats_bytes);
+    if (a.D <= 64) return launch_many<Tag, 2>(a, dtype_index, 0, st);
+    if (a.D <= 128) return launch_many<Tag, 4>(a, dtype_index, 1, st);
+    return launch_many<Tag, 8>(a, dtype_index, 2, st);
 }
 
 }  // namespace
@@ -1187,8 +1019,8 @@ extern "C" size_t spec_score_workspace_size(int batch, int queries, int q_heads,
         const FewPlan p = few_plan(B, kv_heads, R, capacity);
         n = std::max(n, p.stats_bytes + p.held_bytes);
     }
-    const ManyPlan p = many_plan(B, kv_heads, R, capacity);
-    return std::max(n, p.stats_bytes + p.l_bytes);
+    const ManyPlan p = many_plan<Bf16>(B, kv_heads, R, capacity), f = many_plan<F32>(B, kv_heads, R, capacity);
+    return std::max({n, p.stats_bytes + p.l_bytes, f.stats_bytes + f.l_bytes});
 }
 
 extern "C" int spec_cache_score(const void *q, const void *k, spec_dtype_t dtype, int64_t q_request_stride,
@@ -1256,22 +1088,5 @@ extern "C" int spec_cache_score(const void *q, const void *k, spec_dtype_t dtype
         a.held = reinterpret_cast<float *>(static_cast<char *>(workspace) + few.stats_bytes);
         return f32 ? launch_few<F32>(a, 0, stream) : launch_few<Bf16>(a, 1, stream);
     }
-    if (!f32) {
-        const ManyPlan many = many_plan(batch, kv_heads, a.R, capacity);
-        a.part = many.part;
-        a.chunks = many.chunks;
-        a.slots = many.slots;
-        a.minus_l = reinterpret_cast<float *>(static_cast<char *>(workspace) + many.stats_bytes);
-        if (head_dim <= 64) return launch_many<2>(a, 0, stream);
-        if (head_dim <= 128) return launch_many<4>(a, 1, stream);
-        return launch_many<8>(a, 2, stream);
-    }
-    const ScorePlan plan = score_plan(batch, kv_heads, a.R, head_dim, capacity, f32);
-    if (static_cast<int64_t>(batch) * kv_heads * plan.blocks > INT_MAX) return SPEC_EUNSUPPORTED;
-    a.blocks = plan.blocks;
-    a.tile_rows = plan.tile_rows;
-    a.held_rows = plan.held_rows;
-    a.part = plan.part;
-    a.pitch = plan.pitch;
-    return launch_score<F32>(a, plan.smem, 0, stream);
+    return f32 ? launch_many<F32>(a, workspace, 0, stream) : launch_many<Bf16>(a, workspace, 1, stream);
 }

@@ -105,6 +105,20 @@ def test_score_many_rows(sv, B, Q, G, H, D, C, scale):
     check_score(sv, q, k, end - count, end, s, scale, inplace=bool(B % 2), transpose=bool(Q % 2))
 
 
+@pytest.mark.parametrize("B, Q, G, H, D, C, scale", [
+    (2, 40, 7, 1, 128, 900, None), (1, 13, 4, 2, 112, 3000, None), (1, 70, 1, 2, 64, 1025, None), (1, 33, 1, 1, 8, 49, None),
+    (2, 32, 4, 1, 72, 300, -0.3), (1, 64, 2, 1, 256, 260, 0.0), (1, 100, 2, 1, 36, 500, 2.0), (60, 16, 3, 1, 64, 40, None),
+])
+def test_score_many_rows_f32(sv, B, Q, G, H, D, C, scale):
+    q, k, s = make(B + 3 * Q + C, B, Q, G, H, D, C, torch.float32)
+    r = np.random.RandomState(C + Q)
+    end = r.randint(min(Q, C), C + 1, B)
+    end[0] = C
+    count = np.array([min(e, r.randint(0, Q + 1)) for e in end])
+    count[0] = min(Q, C)
+    check_score(sv, q, k, end - count, end, s, scale, inplace=bool(B % 2), transpose=bool(Q % 2))
+
+
 def test_score_many_rows_nan_inf(sv):
     q, k, s = make(8, 1, 20, 4, 3, 64, 400, torch.bfloat16)
     k[0, 1, 150, 3] = float("nan")

@@ -328,7 +328,8 @@ SPECVERIFY_API int spec_plug_tokens(const int32_t *in_tokens, const int32_t *out
  *   scores[w] + (l[v] - m)/T - ln sum_u exp((l[u] - m)/T)   (row w; m its max).
  * The `keep` best candidates are written in order of their scores as exact
  * numbers (they are compared to within fp64 rounding; the fp32 out_scores are
- * rounded afterwards), equal scores by the lower w, then the lower v.  A
+ * within 6e-6 and one rounding of them), equal scores by the lower w, then the
+ * lower v.  A
  * candidate with -inf is none; slots left over get parent and token -1 and
  * score -inf.  A row of nothing but -inf has no candidate (no error).
  * Outputs: out_scores [B][keep] fp32, out_parents [B][keep] (w),

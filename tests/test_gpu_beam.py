@@ -160,6 +160,16 @@ def test_rows_masked_by_the_lowest_value(sv, dtype):
     check(sv, x, s, 9000, 64, 0.25)
 
 
+@pytest.mark.parametrize("T, scale", [(1e-6, 3.0), (1e-4, 3.0), (1.0, 3e4), (1e-3, 1e3), (1e-20, 1.0), (1e6, 3.0)])
+def test_extreme_temperatures_and_logits(sv, T, scale):
+    # products log2(e) l / T from 1e-6 to 1e21: the rounding of the largest must not reach the sums.
+    # (Far larger T bring differences of scores, 1e-6 / T for fp32 logits near 10, below
+    # fp64's step at the scores' size, 2e-15: there the documented order is none.)
+    x, s = rows(7, 2, 3, 3001, torch.float32, scale=scale)
+    check(sv, x, s, 3001, 5, T)
+    check(sv, x.to(torch.bfloat16)[:, :, :3000].contiguous(), s, 3000, 5, T)
+
+
 def test_finished_beams(sv):
     x, s = rows(8, 3, 5, 1500, torch.bfloat16)
     fin = torch.zeros((3, 5), dtype=torch.int32)

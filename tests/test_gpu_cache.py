@@ -314,3 +314,51 @@ def test_evict_streams_and_a_graph(sv):
     torch.cuda.synchronize()
     for a, c, o in runs + [(k1, v1, o1)]:
         assert torch.equal(a, k0) and torch.equal(c, v0) and all(torch.equal(x, y) for x, y in zip(o, o0))
+
+
+# ------------------------------------------------------- offsets past 32 bits
+def test_strides_past_32_bits(sv):
+    # slots 2^27 elements apart: the last one starts 5 * 2^30 elements in
+    step, n = 1 << 27, 40
+    store = torch.empty(step * n, dtype=torch.bfloat16, device="cuda")
+    k = store.as_strided((1, 1, n, 64), (0, 0, step, 1))
+    q, small, s = make(3, 1, 2, 2, 1, 64, n, torch.bfloat16)
+    k.copy_(small)
+    got = sv.spec_cache_score(q.cuda(), k, ints([38]), ints([40]), s.cuda())
+    want = sv.spec_cache_score(q.cuda(), small.cuda(), ints([38]), ints([40]), s.cuda())
+    assert torch.equal(got, want)
+    big = torch.randn((1, 40, 2, 64)).to(torch.bfloat16)      # 80 rows: the sweeps for many
+    got = sv.spec_cache_score(big.cuda(), k, ints([0]), ints([40]), s.cuda())
+    want = sv.spec_cache_score(big.cuda(), small.cuda(), ints([0]), ints([40]), s.cuda())
+    assert torch.equal(got, want)
+    scores, pos = cache(7, 1, 1, n)
+    args = torch.from_numpy(scores).cuda(), ints(pos), ints([n]), 25, 2, 5
+    dense = small.cuda()
+    a = sv.spec_cache_evict(k, None, *[x.clone() if torch.is_tensor(x) else x for x in args])
+    b = sv.spec_cache_evict(dense, None, *[x.clone() if torch.is_tensor(x) else x for x in args])
+    assert torch.equal(k.contiguous(), dense) and torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+    beams = store.as_strided((1, n, 64), (0, step, 1))        # the same rows as beams of one request
+    par = torch.randperm(n, generator=torch.Generator().manual_seed(1)).to(torch.int32)[None].cuda()
+    want = beams[:, par[0].long()].clone()
+    sv.spec_reorder_beams([beams], par)
+    assert torch.equal(beams, want)
+
+
+def test_workspaces_and_devices(sv):
+    q, k, s = make(4, 1, 2, 2, 1, 64, 100, torch.bfloat16)
+    q, k, s = q.cuda(), k.cuda(), s.cuda()
+    need = sv.load_library().spec_score_workspace_size(1, 2, 2, 1, 100)
+    begin, end = ints([98]), ints([100])
+    ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+    a = sv.spec_cache_score(q, k, begin, end, s.clone(), workspace_buf=ws)
+    assert torch.equal(a, sv.spec_cache_score(q, k, begin, end, s.clone()))
+    with pytest.raises(sv.SpecVerifyError):
+        sv.spec_cache_score(q, k, begin, end, s, workspace_buf=ws[:need - 256])
+    with pytest.raises(ValueError):
+        sv.spec_cache_score(q, k.cpu(), begin, end, s)
+    with pytest.raises(ValueError):
+        sv.spec_cache_score(q, k, begin.cpu(), end, s)
+    with pytest.raises(TypeError):
+        sv.spec_cache_score(q.half(), k.half(), begin, end, s)
+    with pytest.raises(ValueError):
+        sv.spec_cache_evict(k, k[:, :, :50], s, ints(np.zeros((1, 1, 100))), end, 10)

@@ -10,7 +10,7 @@
 //  (2) a candidate among the K best lies in one of the at most K items (2048
 //      bf16 or 1024 fp32 entries of a row) whose maxima are the best: an item
 //      that comes before its own item's maximum holds a better candidate.
-// Pass 1 (k_pass1 of sv_verify.cuh) therefore reads every logit once for
+// Pass 1 (the streaming loop of sv_verify.cuh) therefore reads every logit once for
 // (max, sum exp) per item, and the select step re-reads about K items per
 // request, whatever W is.
 //
@@ -33,7 +33,133 @@
 #include "sv_verify.cuh"
 
 namespace sv {
+
+// Beam selection as a mode of pass 1: R = W rows a request, and what its
+// items need beside the shared parameters.
+constexpr int kBeam = 3;
+struct BeamParams : Params {
+    const float *beam_scores;   // [B][W]
+    const int32_t *beam_done;   // [B][W], nullable
+};
+
+// An item of row r of request b; the rows of beams that are not in use or
+// have ended are not read.
+template <class Tag>
+__device__ __forceinline__ Item1 beam_item(const Params &p, unsigned item)
+{
+    const auto &q = static_cast<const BeamParams &>(p);
+    Item1 it;
+    it.b = static_cast<int>(fdiv(item, p.div_req));
+    const unsigned rem = item - static_cast<unsigned>(it.b) * p.div_req.d;
+    it.r = static_cast<int>(fdiv(rem, p.div_s));
+    it.s = static_cast<int>(rem - static_cast<unsigned>(it.r) * p.div_s.d);
+    it.e_begin = it.s * Pass1Shape<Tag>::kItem;
+    it.e_end = min(p.V, it.e_begin + Pass1Shape<Tag>::kItem);
+    const int64_t row = static_cast<int64_t>(it.b) * p.R + it.r;
+    it.active = __ldg(q.beam_scores + row) != -INFINITY && !(q.beam_done && __ldg(q.beam_done + row));
+    it.row = static_cast<const char *>(p.tl) + row * p.stride * static_cast<int64_t>(sizeof(typename Tag::elem));
+    return it;
+}
+template <>
+__device__ __forceinline__ Item1 item1<Bf16, kBeam>(const Params &p, unsigned item, bool)
+{
+    return beam_item<Bf16>(p, item);
+}
+template <>
+__device__ __forceinline__ Item1 item1<F32, kBeam>(const Params &p, unsigned item, bool)
+{
+    return beam_item<F32>(p, item);
+}
+
+// Up to this |m c| the rounding of m c (2^-12 here) is made good by its
+// first-order term, to 2e-8; past it (small temperatures; a lane of nothing
+// but mask values near the type's lowest) the differences are formed first.
+constexpr float kDirectProduct = 8192.f;
+
+// (max, sum 2^((l - max) c)) of a staged item: one FMA and one
+// special-function exponential per entry against the lane's own maximum,
+// four sums, the lanes brought to the warp's maximum.
+template <class Tag>
+__device__ __forceinline__ void reduce_beam_item(const Params &p, unsigned item, int s, const uint4 *slot)
+{
+    constexpr int kVec = Tag::kVec;
+    constexpr int kV = Pass1Shape<Tag>::kVecL;
+    const int lane = threadIdx.x & 31;
+    const int e_begin = s * Pass1Shape<Tag>::kItem;
+    uint4 raw[kV];
+    if (e_begin + Pass1Shape<Tag>::kItem <= p.V) {
+#pragma unroll
+        for (int v = 0; v < kV; ++v) raw[v] = slot[v * 32 + lane];
+    } else {  // the ragged end of a row
+#pragma unroll
+        for (int v = 0; v < kV; ++v) {
+            const int e0 = e_begin + (v * 32 + lane) * kVec;
+            raw[v] = e0 < p.V ? mask_tail<Tag>(slot[v * 32 + lane], p.V - e0)
+                              : make_uint4(Tag::kNegInfWord, Tag::kNegInfWord, Tag::kNegInfWord, Tag::kNegInfWord);
+        }
+    }
+    const float c = p.c;
+    const float m = lane_max<Tag>(raw);
+    const float mc = m == -INFINITY ? 0.f : m * c;  // all -inf: every term is 0
+    const bool direct = fabsf(mc) > kDirectProduct && fabsf(m) < INFINITY;
+    float lsum;
+    if (!direct) {
+        const unsigned long long c2 = f2_pack(c, c), n2 = f2_pack(-mc, -mc);
+        unsigned long long acc[2] = {f2_pack(0.f, 0.f), f2_pack(0.f, 0.f)};
+#pragma unroll
+        for (int v = 0; v < kV; ++v) {
+            float x[kVec];
+            unpack<Tag>(raw[v], x);
+#pragma unroll
+            for (int e = 0; e < kVec; e += 2) {
+                float z0, z1;
+                f2_unpack(f2_fma(f2_pack(x[e], x[e + 1]), c2, n2), z0, z1);
+                acc[(e >> 1) & 1] = f2_add(acc[(e >> 1) & 1], f2_pack(ex2_approx(z0), ex2_approx(z1)));
+            }
+        }
+        float a0, a1, a2, a3;
+        f2_unpack(acc[0], a0, a1);
+        f2_unpack(acc[1], a2, a3);
+        // fl(m c) - m c, exactly, as a factor
+        lsum = ((a0 + a1) + (a2 + a3)) * fmaf(-fmaf(m == -INFINITY ? 0.f : m, c, -mc), 0.693147180559945309f, 1.0f);
+    } else {
+        float a[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int v = 0; v < kV; ++v) {
+            float x[kVec];
+            unpack<Tag>(raw[v], x);
+#pragma unroll
+            for (int e = 0; e < kVec; ++e) a[e & 3] += ex2_approx((x[e] - m) * c);
+        }
+        lsum = (a[0] + a[1]) + (a[2] + a[3]);
+    }
+    const float M = warp_max_nan(m);
+    const float sum = warp_sum(m == -INFINITY ? 0.f : lsum * ex2_approx((m - M) * c));
+    if (lane == 0) __stcg(p.rowpart + item, make_float2(M, sum));
+}
+template <>
+__device__ __forceinline__ void reduce_item1<Bf16, kBeam>(const Params &p, unsigned item, int s, const uint4 *slot)
+{
+    reduce_beam_item<Bf16>(p, item, s, slot);
+}
+template <>
+__device__ __forceinline__ void reduce_item1<F32, kBeam>(const Params &p, unsigned item, int s, const uint4 *slot)
+{
+    reduce_beam_item<F32>(p, item, s, slot);
+}
+
 namespace {
+
+// Pass 1 over the beams' rows: the streaming loop of the other calls.
+template <class Tag>
+__global__ void __launch_bounds__(kThreads, 2) k_beam_pass1(const __grid_constant__ BeamParams p)
+{
+    extern __shared__ uint4 rings[];
+    asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
+    const int warp = threadIdx.x >> 5;
+    pass1_stream<Tag, kBeam>(p, rings + warp * kRing1 * Pass1Shape<Tag>::kSlot, blockIdx.x * kWarps + warp,
+                             gridDim.x * kWarps);
+}
 
 constexpr int kBeamThreads = 512;
 constexpr int kBeamWarps = kBeamThreads / 32;
@@ -244,7 +370,7 @@ __device__ __forceinline__ double exact_sum(const Params &p, int b, int w, float
 // Select: one block per request, after pass 1.
 template <class Tag>
 __global__ void __launch_bounds__(kBeamThreads)
-    k_beam_select(const __grid_constant__ Params p, const __grid_constant__ BeamArgs a)
+    k_beam_select(const __grid_constant__ BeamParams p, const __grid_constant__ BeamArgs a)
 {
     extern __shared__ Cand cand[];
     __shared__ BeamRows rw;
@@ -590,7 +716,7 @@ constexpr int kCandMin = 1024;
 size_t cand_count(int K) { return std::max(kCandMin, K * K) + SPEC_MAX_BEAMS; }
 
 template <class Tag>
-int launch_beam(Params &p, BeamArgs &a, int dtype_index, cudaStream_t st)
+int launch_beam(BeamParams &p, BeamArgs &a, int dtype_index, cudaStream_t st)
 {
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return SPEC_ECUDA;
@@ -599,9 +725,9 @@ int launch_beam(Params &p, BeamArgs &a, int dtype_index, cudaStream_t st)
         std::lock_guard<std::mutex> lock(g_beam_mu);
         if (g_beam_blocks[dev][dtype_index] < 1) {
             int n = 0;
-            if (cudaFuncSetAttribute(k_pass1<Tag, kBeam, 2>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+            if (cudaFuncSetAttribute(k_beam_pass1<Tag>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                      static_cast<int>(kRingBytes)) != cudaSuccess ||
-                cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, k_pass1<Tag, kBeam, 2>, kThreads, kRingBytes) !=
+                cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, k_beam_pass1<Tag>, kThreads, kRingBytes) !=
                     cudaSuccess ||
                 n < 1)
                 return SPEC_ECUDA;
@@ -627,7 +753,7 @@ int launch_beam(Params &p, BeamArgs &a, int dtype_index, cudaStream_t st)
     // (rows of 128256 bf16: 32 x 16 42.7 us static, 48.7 with a claimed tail;
     // 128 x 16 139.5 and 143.1; 256 x 4 65.8 and 70.5)
     p.nAs = p.nA;
-    k_pass1<Tag, kBeam, 2><<<static_cast<unsigned>(blocks), kThreads, kRingBytes, st>>>(p);
+    k_beam_pass1<Tag><<<static_cast<unsigned>(blocks), kThreads, kRingBytes, st>>>(p);
     if (cudaGetLastError() != cudaSuccess) return SPEC_ECUDA;
     a.cap = static_cast<int>(cand_count(a.keep));
     cudaLaunchConfig_t cfg = {};
@@ -684,8 +810,8 @@ extern "C" int spec_beam_select(const void *logits, spec_dtype_t dtype, int64_t 
     const int64_t nA = static_cast<int64_t>(batch) * beams * S;
     if (nA >= (int64_t(1) << 31) || static_cast<int64_t>(batch) * keep > INT_MAX) return SPEC_EUNSUPPORTED;
 
-    Params p;
-    std::memset(&p, 0, sizeof p);
+    BeamParams p;
+    std::memset(static_cast<void *>(&p), 0, sizeof p);
     p.tl = logits;
     p.stride = row_stride;
     p.B = batch;

@@ -301,7 +301,7 @@ struct __align__(64) ReqInfo {
                      //   certain from fp32 (residual only)
 };
 
-enum : int { kLinear = 0, kTreeStochastic = 1, kTreeGreedy = 2, kBeam = 3 };
+enum : int { kLinear = 0, kTreeStochastic = 1, kTreeGreedy = 2 };
 
 struct Params {
     const void *tl;          // target logits
@@ -309,8 +309,6 @@ struct Params {
     int64_t stride;          // row pitch in elements
     const int32_t *tokens;   // linear: draft tokens [B][k]; tree: node tokens [B][N]
     const int32_t *parents;  // tree only
-    const float *beam_scores;   // beam selection only, [B][R]
-    const int32_t *beam_done;   // beam selection only, [B][R], nullable
     int B, k, N, max_depth, V;
     int R;                   // rows per request streamed by pass 1
     int S;                   // pass-1 items per row

@@ -179,9 +179,6 @@ struct Pass1Shape {
 constexpr int kRing1 = 3;  // ring slots per warp: one reduced, two in flight
 constexpr size_t kRingBytes = sizeof(uint4) * kRing1 * 32 * 8 * kWarps;
 constexpr unsigned kNoItem = 0xFFFFFFFFu;
-// Beam selection: up to this |m c| the rounding of m c (2^-12 here) is made
-// good by its first-order term, to 2e-8.
-constexpr float kDirectProduct = 8192.f;
 
 struct Item1 {
     const char *row;
@@ -224,10 +221,6 @@ __device__ __forceinline__ Item1 item1(const Params &p, unsigned item, bool chec
             base = p.dl;
             row = static_cast<int64_t>(b) * p.k + (r - p.k - 1);
         }
-    } else if (MODE == kBeam) {  // the rows of beams in use that have not ended
-        base = p.tl;
-        row = static_cast<int64_t>(b) * p.R + r;
-        it.active = __ldg(p.beam_scores + row) != -INFINITY && !(p.beam_done && __ldg(p.beam_done + row));
     } else if (r < p.N) {
         base = p.tl;
         row = static_cast<int64_t>(b) * p.N + r;
@@ -395,25 +388,7 @@ __device__ __forceinline__ void reduce_item1(const Params &p, unsigned item, int
         const float lsum = (acc[0] + acc[1]) + (acc[2] + acc[3]);
         const float M = warp_max_nan(m);
         float sr = 0.f;
-        bool direct = false;
-        if (MODE == kBeam) {
-            // m c large or out of range (small temperatures; a lane of nothing
-            // but mask values near the type's lowest): its rounding is no
-            // longer small, so the differences first
-            direct = fabsf(mc) > kDirectProduct && fabsf(m) < INFINITY;
-            if (direct) {
-                float sum[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                for (int v = 0; v < kV; ++v) {
-                    float x[kVec];
-                    unpack<Tag>(raw[v], x);
-#pragma unroll
-                    for (int e = 0; e < kVec; ++e) sum[e & 3] += ex2_approx((x[e] - m) * c);
-                }
-                sr = ((sum[0] + sum[1]) + (sum[2] + sum[3])) * ex2_approx((m - M) * c);
-            }
-        }
-        if (m != -INFINITY && !direct) {
+        if (m != -INFINITY) {
             const float d = -fmaf(m, c, nmc);  // fl(m c) - m c, exactly
             sr = lsum * ex2_approx((m - M) * c) * fmaf(d, 0.693147180559945309f, 1.0f);
         }

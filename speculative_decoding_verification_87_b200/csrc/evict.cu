@@ -323,12 +323,13 @@ __global__ void __launch_bounds__(256) k_evict_move(const __grid_constant__ Evic
 // Heads of up to kSmallSlots slots: one block a head, the keys in registers
 // (slot j * threads + tid), the budget-th largest by a search with three
 // pivots a step, two bits each; it ends early where a pivot has exactly
-// `budget` keys above.  With kFused the block also moves the rows.
+// `budget` keys above.  With kFused the block also moves the rows.  (8 heads
+// of 4000 slots 9.0 us, 256 of 2057 12.4; the cluster form takes 17 and 19.)
 constexpr int kSmallThreads = 512;
 constexpr int kSmallWarps = kSmallThreads / 32;
 constexpr int kSmallKeys = 8;
 constexpr int kSmallSlots = kSmallThreads * kSmallKeys;
-constexpr int kFusedMoves = 64;  // moves a head can have in the fused form
+constexpr int kFusedMoves = kSmallSlots / 2;  // at most min(budget, capacity - budget)
 
 template <class T, bool kFused>
 __global__ void __launch_bounds__(kSmallThreads, 2) k_evict_small(const __grid_constant__ EvictArgs a)
@@ -549,15 +550,19 @@ int cluster_blocks(int C)
     return n;
 }
 
-// Launches: small caches in one block a head (with few moves and lengths
-// that nothing overwrites while other heads read them, the moves as well),
-// large ones in a cluster a head, then the moves as a programmatic dependent.
+// Launches: small caches in one block a head, large ones in a cluster a head,
+// then the moves as a programmatic dependent.
 template <class T>
 int launch_evict(const EvictArgs &a, cudaStream_t stream)
 {
     const int64_t heads = static_cast<int64_t>(a.B) * a.H;
     if (a.C <= kSmallSlots) {
-        if (a.most <= kFusedMoves && a.out_lens != a.lens) {
+        // One kernel while a block a head moves its rows as fast as the whole
+        // GPU would: few moves, or heads for most SMs (32 heads, one kernel /
+        // two: 128 moves 9.9 / 10.5 us, 256 12.0 / 10.9; 128 heads: 128 moves
+        // 10.5 / 12.1, 2048 48 / 50; 512 heads: 2048 moves 131 / 166).  The
+        // lengths must not be overwritten while other heads read them.
+        if ((a.most <= 128 || heads >= 128) && a.out_lens != a.lens) {
             k_evict_small<T, true><<<static_cast<unsigned>(heads), kSmallThreads, 0, stream>>>(a);
             return cudaGetLastError() == cudaSuccess ? SPEC_OK : SPEC_ECUDA;
         }

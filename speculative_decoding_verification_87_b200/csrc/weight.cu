@@ -288,10 +288,10 @@ __device__ __forceinline__ void products(const Slots<Tag, NB> &k, const uint4 *s
 // Decoding and small verifications: reading the keys bounds the step, so they
 // are read once.  k_score_few forms the products, stores them and the
 // statistics of its chunk; k_score_sum merges the statistics and adds up the
-// weights from the stored products.  They are written and read once, 8 bytes
-// per product, which is less than a second read of the keys while
-// 8 R < D * element size.  No cluster, no wait: a head of any length spreads
-// over the whole GPU.
+// weights from the stored products.  No cluster, no wait: a head of any length
+// spreads over the whole GPU.  (32 requests of 2050 to 4096 slots, 8 heads of
+// 4 rows, D = 128 bf16, 203 MB of keys: 46 us, 4.4 TB/s; of these the keys'
+// read takes about 36 and its start and the second kernel the rest.)
 constexpr int kFewRows = 32;
 
 // Products and statistics of one chunk of slots: grid (chunk, head).  A warp
@@ -826,9 +826,19 @@ int64_t ceil_div(int64_t x, int64_t y) { return (x + y - 1) / y; }
 size_t align_up(size_t x) { return (x + kScoreAlign - 1) / kScoreAlign * kScoreAlign; }
 
 std::mutex g_score_mu;
-// Few rows: while storing the products (8 bytes each, there and back) moves
-// less than a second read of the keys.
-bool few_rows(bool f32, int R, int D) { return R <= kFewRows && 8 * R < D * (f32 ? 4 : 2); }
+// Few rows, for the form that stores its products: while that moves no more
+// (8 bytes a product, there and back) than a second read of the keys.  (bf16,
+// half a million slots, stored / swept twice: R = 16, D = 128 40 / 67 us; R =
+// 32, D = 128 57 / 73; R = 16, D = 64 28 / 37; R = 32, D = 64 46 / 45.)  Below
+// a quarter million bf16 slots the keys' second read comes from L2 and only
+// half as many rows pay (64 K slots, D = 128: R = 8 11.7 / 13.8 us, R = 16
+// 15.8 / 13.9, R = 24 21.0 / 15.4).  In fp32 the products cost six times as
+// much and are not formed twice (128 K slots: R = 32, D = 128 45 / 85 us).
+bool few_rows(bool f32, int R, int D, int64_t slots)
+{
+    if (f32) return R <= kFewRows && 2 * R <= D;
+    return slots >= 1 << 18 ? R <= kFewRows && 4 * R <= D : R <= 16 && 8 * R <= D;
+}
 
 struct FewPlan {
     int part, chunks, pitch;
@@ -1035,7 +1045,8 @@ extern "C" int spec_cache_score(const void *q, const void *k, spec_dtype_t dtype
         head_dim < 1 || capacity < 1)
         return SPEC_EINVAL;
     if (dtype != SPEC_F32 && dtype != SPEC_BF16) return SPEC_EINVAL;
-    if (!std::isfinite(scale)) return SPEC_EINVAL;
+    const float scale2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634074);
+    if (!std::isfinite(scale2)) return SPEC_EINVAL;
     const int vec = dtype == SPEC_BF16 ? 8 : 4;
     if (head_dim % vec != 0) return SPEC_EALIGN;
     if (head_dim < 8 || head_dim > SPEC_MAX_HEAD_DIM || batch > 65535 || kv_heads > 65535 ||
@@ -1075,12 +1086,12 @@ extern "C" int spec_cache_score(const void *q, const void *k, spec_dtype_t dtype
     a.D = head_dim;
     a.C = capacity;
     a.R = a.Q * a.G;
-    a.scale2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634074);
+    a.scale2 = scale2;
     a.in = scores;
     a.out = out_scores;
     a.status = status;
     a.stats = static_cast<float2 *>(workspace);
-    if (few_rows(f32, a.R, head_dim)) {
+    if (few_rows(f32, a.R, head_dim, static_cast<int64_t>(batch) * kv_heads * capacity)) {
         const FewPlan few = few_plan(batch, kv_heads, a.R, capacity);
         a.part = few.part;
         a.chunks = few.chunks;

@@ -119,6 +119,18 @@ def test_score_many_rows_f32(sv, B, Q, G, H, D, C, scale):
     check_score(sv, q, k, end - count, end, s, scale, inplace=bool(B % 2), transpose=bool(Q % 2))
 
 
+@pytest.mark.parametrize("dtype, B, Q, G, H, D, C", [
+    # rows and slots on either side of the choice between stored products and a second sweep
+    (torch.bfloat16, 8, 5, 4, 8, 128, 4096), (torch.bfloat16, 8, 5, 4, 8, 128, 4095), (torch.bfloat16, 8, 2, 16, 8, 128, 4096),
+    (torch.bfloat16, 2, 1, 17, 16, 64, 8192), (torch.bfloat16, 3, 2, 8, 2, 128, 515), (torch.bfloat16, 3, 17, 1, 2, 128, 515),
+    (torch.bfloat16, 1, 16, 1, 2, 256, 700), (torch.float32, 1, 16, 2, 2, 64, 700), (torch.float32, 1, 11, 3, 2, 64, 700),
+])
+def test_score_between_few_and_many_rows(sv, dtype, B, Q, G, H, D, C):
+    q, k, s = make(B + 5 * Q + C, B, Q, G, H, D, C, dtype)
+    end = np.array([C - 700 * b // B * (C > 1000) for b in range(B)])
+    check_score(sv, q, k, end - np.minimum(Q, end), end, s)
+
+
 def test_score_many_rows_nan_inf(sv):
     q, k, s = make(8, 1, 20, 4, 3, 64, 400, torch.bfloat16)
     k[0, 1, 150, 3] = float("nan")
@@ -235,6 +247,18 @@ def test_evict(sv, B, H, C, budget, sinks, recent):
     lens[0] = C
     check_evict(sv, scores, pos, lens, budget, sinks, recent)
     check_evict(sv, scores, pos, lens, budget, sinks, recent, inplace=True, transpose=True)
+
+
+@pytest.mark.parametrize("B, H, C, budget", [
+    # moves and heads on either side of the choice between one kernel and two
+    (2, 2, 400, 272), (2, 2, 400, 271), (16, 8, 900, 450), (127, 1, 900, 450), (16, 8, 4096, 2048), (130, 1, 300, 20),
+])
+def test_evict_between_one_kernel_and_two(sv, B, H, C, budget):
+    scores, pos = cache(C + budget + B, B, H, C)
+    lens = np.random.RandomState(B).randint(0, C + 1, B)
+    lens[0] = C
+    check_evict(sv, scores, pos, lens, budget, 2, 10)
+    check_evict(sv, scores, pos, lens, budget, 2, 10, inplace=True)
 
 
 @pytest.mark.parametrize("dtype, D, Dv", [(torch.float32, 1, 3), (torch.bfloat16, 5, 16), (torch.int8, 7, 1),

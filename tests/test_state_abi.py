@@ -68,6 +68,18 @@ def test_reorder_refusals(lib, want, change):
     assert _beams(lib, **change) == want
 
 
+def test_a_state_that_comes_twice_is_refused(lib):
+    assert _beams(lib, states=(0x1000, 0x2000, 0x1000), n=3) == EINVAL
+    assert _path(lib, states=(0x1000, 0x1000), n=2) == EINVAL
+
+
+def test_select_in_place_needs_as_many_kept_as_held(lib):
+    assert _select(lib, keep=3, out=0x2000) == EINVAL
+    assert _select(lib, keep=5, out=0x2000) == EINVAL
+    # keep == beams gets past that check, to the workspace's
+    assert _select(lib, keep=4, out=0x2000, ws=0) == EWORKSPACE
+
+
 def _path(lib, **kw):
     a = dict(states=(0x1000, 0x2000), n=2, request=4096, segments=2, segment=512, unit=16, cap=32,
              base=0x8000, path=0x9000, batch=2, nodes=10, width=5, lens=0xa000)
@@ -221,3 +233,13 @@ def test_reference_evict_by_hand():
     # position 0 (sink) and 5 (newest) stay, then scores 5 and 3: slot 2 is given up for slot 5
     k2, _, s2, p2, n = ref.evict(k, k, s, p, np.array([6]), 4, 1, 1)
     assert k2[0, 0, :, 0].tolist() == [0, 1, 5, 3, 4, 5] and p2[0, 0, :4].tolist() == [0, 1, 5, 3] and n.tolist() == [4]
+
+
+@pytest.mark.parametrize("want, change", [
+    (EINVAL, dict(kh=0)), (EINVAL, dict(kr=0)), (EINVAL, dict(vh=0)), (EINVAL, dict(vr=0)),       # expanded heads, requests
+    (EINVAL, dict(kh=2047)), (EINVAL, dict(kr=8191)), (EINVAL, dict(kh=1 << 42, kr=1 << 42)),
+    (OK, dict(kh=128, ks=512)), (OK, dict(kr=128, kh=256, ks=1024)), (OK, dict(vh=0, heads=1)), (OK, dict(v=0, vh=0)),
+])
+def test_evict_rows_that_overlap_are_refused(lib, want, change):
+    # what gets past the check stops at the workspace's
+    assert _evict(lib, ws=0, **change) == (EWORKSPACE if want == OK else want)

@@ -1,4 +1,5 @@
-"""B200-native speculative-decoding verification sampler.
+"""B200-native speculative-decoding verification sampler, with the beam
+selection, state reordering and cache eviction steps around it.
 
 The compute path is ``libspecverify.so`` (hand-written sm_100a CUDA kernels
 behind a C ABI, declared in ``include/specverify.h``).  ``binding`` marshals

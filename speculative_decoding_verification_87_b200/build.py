@@ -3,8 +3,9 @@
     python -m speculative_decoding_verification_87_b200.build [--force]
 
 The library is built from csrc/*.cu (specverify.cu with its headers,
-noalloc.cu, and walk.cu with sv_walk.cuh), compiled for sm_100a only,
-with static cudart and -lineinfo.
+noalloc.cu, walk.cu with sv_walk.cuh, plug.cu, shard.cu, beam.cu, reorder.cu,
+weight.cu and evict.cu), compiled for sm_100a only, with static cudart and
+-lineinfo.
 """
 import glob
 import os

@@ -10,6 +10,7 @@ Build it with ``python -m speculative_decoding_verification_87_b200.build``.
 """
 import array
 import ctypes
+import functools
 import os
 import threading
 
@@ -159,7 +160,7 @@ def _need_cuda(name, t, dtype=None, shape=None):
         raise ValueError(f"{name} must be contiguous")
     if dtype is not None and t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if shape is not None and tuple(t.shape) != tuple(shape):
+    if shape is not None and t.shape != shape and tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
 
 
@@ -504,6 +505,12 @@ def _one_device(dev, *named):
             raise ValueError(f"{name} is on {t.device}, not on {dev}")
 
 
+@functools.lru_cache(maxsize=256)
+def _bytes(call, *sizes):
+    """A workspace size of the library by its function's name."""
+    return getattr(load_library(), call)(*sizes)
+
+
 def _scratch(need, buf, dev):
     """A workspace of `need` bytes: the caller's, or a new one (the caching
     allocator's blocks are 512-byte aligned; a captured graph gets its own)."""
@@ -553,7 +560,7 @@ def spec_beam_select(logits, scores, vocab, keep, temperature=1.0, finished=None
         code = _dtype_code(logits)
         ws = None
         if B > 0:
-            need = lib.spec_beam_workspace_size(B, W, vocab)
+            need = _bytes("spec_beam_workspace_size", B, W, vocab)
             ws = _scratch(need, workspace_buf, dev) if need else workspace_buf
         rc = lib.spec_beam_select(
             _at(logits), code, stride, _at(scores), _at(finished), int(end_token), B, W, vocab,
@@ -578,34 +585,41 @@ def _one_stride(sizes, strides):
     return count, step
 
 
-def _state_layout(states, lead, axis):
-    """The common layout of `states`, whose first `lead` dimensions are the
-    request (and the beam): (segments, segment stride, unit bytes, capacity)
-    and the device.  axis: the dimension of the units (positions), or None
-    where a whole state is one unit."""
-    t = states[0]
-    if t.dim() < lead or (axis is not None and not lead <= axis < t.dim()):
+@functools.lru_cache(maxsize=256)
+def _layout(shape, stride, e, lead, axis):
+    """Of a state of these sizes and strides and e bytes an element:
+    (segments, segment stride, unit bytes, capacity).  Kept per layout: a
+    serving loop has a few and asks for them at every step."""
+    if len(shape) < lead or (axis is not None and not lead <= axis < len(shape)):
         raise ValueError("axis must be a dimension after the request's and the beam's")
-    if not t.is_cuda:
-        raise ValueError("the states must be CUDA tensors")
-    e = t.element_size()
-    shape, stride, dtype, dev = t.shape, t.stride(), t.dtype, t.get_device()
-    for x in states:
-        if x.shape != shape or x.stride() != stride or x.dtype is not dtype or x.get_device() != dev:
-            raise ValueError("the states must share device, dtype, shape and strides")
     inner = lead if axis is None else axis + 1
     whole = _one_stride(shape[inner:], stride[inner:])
     if whole is None or (whole[0] > 1 and whole[1] != 1):
         raise ValueError("the dimensions of a unit must be contiguous")
     unit = whole[0] * e
     if axis is None:
-        return 1, 0, unit, 1, t.device
+        return 1, 0, unit, 1
     if shape[axis] > 1 and stride[axis] * e != unit:
         raise ValueError("the units must follow one another")
     seg = _one_stride(shape[lead:axis], stride[lead:axis])
     if seg is None:
         raise ValueError("the dimensions before the units must have one stride")
-    return seg[0], seg[1] * e, unit, shape[axis], t.device
+    return seg[0], seg[1] * e, unit, shape[axis]
+
+
+def _state_layout(states, lead, axis):
+    """The common layout of `states`, whose first `lead` dimensions are the
+    request (and the beam): (segments, segment stride, unit bytes, capacity)
+    and the device.  axis: the dimension of the units (positions), or None
+    where a whole state is one unit."""
+    t = states[0]
+    if not t.is_cuda:
+        raise ValueError("the states must be CUDA tensors")
+    shape, stride, dtype, dev = t.shape, t.stride(), t.dtype, t.get_device()
+    for x in states:
+        if x.shape != shape or x.stride() != stride or x.dtype is not dtype or x.get_device() != dev:
+            raise ValueError("the states must share device, dtype, shape and strides")
+    return *_layout(shape, stride, t.element_size(), lead, axis), t.device
 
 
 def _pointers(states):
@@ -725,7 +739,7 @@ def spec_cache_score(q, k, begin, end, scores, scale=None, out_scores=None, stat
     with _On(dev, stream) as handle:
         ws = None
         if B > 0:
-            need = lib.spec_score_workspace_size(B, Q, Hq, H, cap)
+            need = _bytes("spec_score_workspace_size", B, Q, Hq, H, cap)
             ws = _scratch(need, workspace_buf, dev) if need else workspace_buf
         rc = lib.spec_cache_score(
             _at(q), _at(k), _dtype_code(q), q.stride(0), q.stride(1), q.stride(2), k.stride(0),
@@ -775,7 +789,7 @@ def spec_cache_evict(k, v, scores, positions, lens, budget, sinks=0, recent=0, o
                     ("workspace_buf", workspace_buf))
         ws = None
         if B > 0:
-            need = lib.spec_evict_workspace_size(B, H, cap, int(budget))
+            need = _bytes("spec_evict_workspace_size", B, H, cap, int(budget))
             ws = _scratch(need, workspace_buf, dev) if need else workspace_buf
         rc = lib.spec_cache_evict(
             _at(k), _at(v), *layout(k), *(layout(v) if v is not None else (0, 0, 0, 0)),

@@ -29,7 +29,7 @@ constexpr int kClusterMax = 8;
 constexpr int kSliceMax = SPEC_MAX_SLOTS / kClusterMax;  // keys of a block: 128 KB at most
 constexpr int kBins = 2048;                              // 11 bits a pass
 constexpr unsigned kAll = 0xFFFFFFFFu;
-constexpr int kMoveGroup = 8;                            // rows a warp moves at a time
+constexpr int kMoveGroup = 4;                            // rows a warp moves at a time
 
 struct EvictArgs {
     char *k, *v;

@@ -302,8 +302,9 @@ __device__ __forceinline__ void move_rows(const EvictArgs &a, int64_t head, cons
     }
 }
 
-// Move: kMoveGroup moves a warp (grid x: moves, y: heads), so that a warp has
-// eight rows in flight.  (16 heads, about 3600 moves each, 59 MB: 22 us.)
+// Move: kMoveGroup moves a warp (grid x: moves, y: heads).  (256 heads, 2048
+// moves of two 256-byte rows each, pick and moves: 148 us with four rows a
+// warp, 182 with eight, whose registers leave half the warps, 177 with two.)
 template <class T>
 __global__ void __launch_bounds__(256) k_evict_move(const __grid_constant__ EvictArgs a)
 {
@@ -576,9 +577,10 @@ int launch_evict(const EvictArgs &a, cudaStream_t stream)
     if (a.C <= kSmallSlots) {
         // One kernel while a block a head moves its rows as fast as the whole
         // GPU would: few moves, or heads for most SMs (32 heads, one kernel /
-        // two: 128 moves 9.9 / 10.5 us, 256 12.0 / 10.9; 128 heads: 128 moves
-        // 10.5 / 12.1, 2048 48 / 50; 512 heads: 2048 moves 131 / 166).  The
-        // lengths must not be overwritten while other heads read them.
+        // two: 128 moves 9.6 / 10.5 us, 256 11.9 / 10.5; 128 heads: 128 moves
+        // 10.4 / 12.0, 512 16.0 / 18.6, 2048 42 / 39; 512 heads: 2048 moves
+        // 119 / 137).  The lengths must not be overwritten while other heads
+        // read them.
         if ((a.most <= 128 || heads >= 128) && a.out_lens != a.lens) {
             k_evict_small<T, true><<<static_cast<unsigned>(heads), kSmallThreads, 0, stream>>>(a);
             return cudaGetLastError() == cudaSuccess ? SPEC_OK : SPEC_ECUDA;

@@ -476,10 +476,11 @@ class _On:
                 raise ValueError(f"stream is on {stream.device}, the tensors on {dev}")
             self.outer, self.handle = torch.cuda.stream(stream), stream.cuda_stream
         else:
-            if dev.index != torch.cuda.current_device():
+            if dev.index != torch._C._cuda_getDevice():
                 self.outer = torch.cuda.device(dev)
             # the handle alone: torch.cuda.current_stream() makes a Stream
-            # object for it, 2 us of a 10 us call
+            # object for it, 2 us of a 10 us call (and as the tensors exist,
+            # CUDA is up, which torch.cuda.current_device() would look at)
             self.handle = torch._C._cuda_getCurrentRawStream(dev.index)
 
     def __enter__(self):
@@ -497,12 +498,12 @@ def _at(t):
     return None if t is None else t.data_ptr()
 
 
-def _one_device(dev, *named):
-    """(name, tensor or None) pairs: all on `dev`."""
-    i = dev.index
-    for name, t in named:
-        if t is not None and t.get_device() != i:
-            raise ValueError(f"{name} is on {t.device}, not on {dev}")
+def _need(i, name, t, dtype, shape=None):
+    """_need_cuda on device i; one comparison of each kind where all is well."""
+    if (t is None or t.get_device() != i or t.dtype is not dtype or (shape is not None and t.shape != shape)
+            or not t.is_contiguous()):
+        _need_cuda(name, t, dtype, shape)
+        raise ValueError(f"{name} is on {t.device}, not on cuda:{i}")
 
 
 @functools.lru_cache(maxsize=256)
@@ -515,7 +516,7 @@ def _scratch(need, buf, dev):
     """A workspace of `need` bytes: the caller's, or a new one (the caching
     allocator's blocks are 512-byte aligned; a captured graph gets its own)."""
     if buf is not None:
-        _need_cuda("workspace_buf", buf, torch.uint8)
+        _need(dev.index, "workspace_buf", buf, torch.uint8)
         return buf
     if need == 0:
         raise ValueError("invalid workspace request")
@@ -534,9 +535,10 @@ def spec_beam_select(logits, scores, vocab, keep, temperature=1.0, finished=None
     B, W, stride = logits.shape
     keep = int(keep)
     dev = logits.device
-    _need_cuda("scores", scores, torch.float32, (B, W))
+    i = dev.index
+    _need(i, "scores", scores, torch.float32, (B, W))
     if finished is not None:
-        _need_cuda("finished", finished, torch.int32, (B, W))
+        _need(i, "finished", finished, torch.int32, (B, W))
     with _On(dev, stream) as handle:
         if out_scores is None:
             out_scores = torch.empty((B, keep), dtype=torch.float32, device=dev)
@@ -546,16 +548,13 @@ def spec_beam_select(logits, scores, vocab, keep, temperature=1.0, finished=None
             out_tokens = torch.empty((B, keep), dtype=torch.int32, device=dev)
         if out_finished is None and finished is not None:
             out_finished = torch.empty((B, keep), dtype=torch.int32, device=dev)
-        _need_cuda("out_scores", out_scores, torch.float32, (B, keep))
-        for name, t in (("out_parents", out_parents), ("out_tokens", out_tokens)):
-            _need_cuda(name, t, torch.int32, (B, keep))
+        _need(i, "out_scores", out_scores, torch.float32, (B, keep))
+        _need(i, "out_parents", out_parents, torch.int32, (B, keep))
+        _need(i, "out_tokens", out_tokens, torch.int32, (B, keep))
         if out_finished is not None:
-            _need_cuda("out_finished", out_finished, torch.int32, (B, keep))
+            _need(i, "out_finished", out_finished, torch.int32, (B, keep))
         if status is not None:
-            _need_cuda("status", status, torch.int32)
-        _one_device(dev, ("scores", scores), ("finished", finished), ("out_scores", out_scores),
-                    ("out_parents", out_parents), ("out_tokens", out_tokens), ("out_finished", out_finished),
-                    ("status", status), ("workspace_buf", workspace_buf))
+            _need(i, "status", status, torch.int32)
         lib = load_library()
         code = _dtype_code(logits)
         ws = None
@@ -647,12 +646,10 @@ def spec_reorder_beams(states, parents, axis=None, begin=None, end=None, status=
         raise ValueError(f"parents must have {states[0].shape[0]} rows, got {B}")
     if axis is None and (begin is not None or end is not None):
         raise ValueError("begin and end need axis")
-    for name, t in (("begin", begin), ("end", end)):
+    _need(dev.index, "parents", parents, torch.int32)
+    for name, t in (("begin", begin), ("end", end), ("status", status)):
         if t is not None:
-            _need_cuda(name, t, torch.int32, (B,))
-    if status is not None:
-        _need_cuda("status", status, torch.int32)
-    _one_device(dev, ("parents", parents), ("begin", begin), ("end", end), ("status", status))
+            _need(dev.index, name, t, torch.int32, None if t is status else (B,))
     e = states[0].element_size()
     addresses = _pointers(states)
     with _On(dev, stream) as handle:
@@ -680,15 +677,15 @@ def spec_commit_path(states, base, path, num_nodes, axis, out_lens=None, status=
         segments, seg_stride, unit, cap, dev = _state_layout(states, 1, axis)
         if states[0].shape[0] != B:
             raise ValueError(f"path must have {states[0].shape[0]} rows, got {B}")
+    _need(dev.index, "path", path, torch.int32)
     if base is not None:
-        _need_cuda("base", base, torch.int32, (B,))
+        _need(dev.index, "base", base, torch.int32, (B,))
     with _On(dev, stream) as handle:
         if out_lens is None:
             out_lens = torch.empty((B,), dtype=torch.int32, device=dev)
-        _need_cuda("out_lens", out_lens, torch.int32, (B,))
+        _need(dev.index, "out_lens", out_lens, torch.int32, (B,))
         if status is not None:
-            _need_cuda("status", status, torch.int32)
-        _one_device(dev, ("base", base), ("path", path), ("out_lens", out_lens), ("status", status))
+            _need(dev.index, "status", status, torch.int32)
         step = states[0].stride(0) * states[0].element_size() if states else cap
         addresses = _pointers(states)
         rc = load_library().spec_commit_path(
@@ -725,15 +722,16 @@ def spec_cache_score(q, k, begin, end, scores, scale=None, out_scores=None, stat
     if k.dtype != q.dtype or tuple(k.shape) != (B, H, cap, D):
         raise ValueError(f"k must be [{B}][kv_heads][capacity][{D}] of {q.dtype}, got {tuple(k.shape)} {k.dtype}")
     dev = q.device
-    _need_cuda("begin", begin, torch.int32, (B,))
-    _need_cuda("end", end, torch.int32, (B,))
-    _need_cuda("scores", scores, torch.float32, (B, H, cap))
+    i = dev.index
+    if k.get_device() != i:
+        raise ValueError(f"k is on {k.device}, not on {dev}")
+    _need(i, "begin", begin, torch.int32, (B,))
+    _need(i, "end", end, torch.int32, (B,))
+    _need(i, "scores", scores, torch.float32, (B, H, cap))
     out_scores = scores if out_scores is None else out_scores
-    _need_cuda("out_scores", out_scores, torch.float32, (B, H, cap))
+    _need(i, "out_scores", out_scores, torch.float32, (B, H, cap))
     if status is not None:
-        _need_cuda("status", status, torch.int32)
-    _one_device(dev, ("k", k), ("begin", begin), ("end", end), ("scores", scores), ("out_scores", out_scores), ("status", status),
-                ("workspace_buf", workspace_buf))
+        _need(i, "status", status, torch.int32)
     scale = D ** -0.5 if scale is None else float(scale)
     lib = load_library()
     with _On(dev, stream) as handle:
@@ -742,8 +740,7 @@ def spec_cache_score(q, k, begin, end, scores, scale=None, out_scores=None, stat
             need = _bytes("spec_score_workspace_size", B, Q, Hq, H, cap)
             ws = _scratch(need, workspace_buf, dev) if need else workspace_buf
         rc = lib.spec_cache_score(
-            _at(q), _at(k), _dtype_code(q), q.stride(0), q.stride(1), q.stride(2), k.stride(0),
-            k.stride(1), k.stride(2), _at(begin), _at(end), B, Q, Hq, H, D, cap, scale,
+            _at(q), _at(k), _dtype_code(q), *q.stride()[:3], *k.stride()[:3], _at(begin), _at(end), B, Q, Hq, H, D, cap, scale,
             _at(scores), _at(out_scores), _at(status), _at(ws),
             0 if ws is None else ws.numel(), handle)
     _check(rc, "spec_cache_score")
@@ -761,32 +758,32 @@ def spec_cache_evict(k, v, scores, positions, lens, budget, sinks=0, recent=0, o
     _inner_contiguous("k", k, 4)
     B, H, cap, _ = k.shape
     dev = k.device
+    i = dev.index
     if v is not None:
         _inner_contiguous("v", v, 4)
         if tuple(v.shape[:3]) != (B, H, cap):
             raise ValueError(f"v must be [{B}][{H}][{cap}][D], got {tuple(v.shape)}")
-    _need_cuda("scores", scores, torch.float32, (B, H, cap))
-    _need_cuda("positions", positions, torch.int32, (B, H, cap))
-    _need_cuda("lens", lens, torch.int32, (B,))
+        if v.get_device() != i:
+            raise ValueError(f"v is on {v.device}, not on {dev}")
+    _need(i, "scores", scores, torch.float32, (B, H, cap))
+    _need(i, "positions", positions, torch.int32, (B, H, cap))
+    _need(i, "lens", lens, torch.int32, (B,))
     out_scores = scores if out_scores is None else out_scores
     out_positions = positions if out_positions is None else out_positions
-    _need_cuda("out_scores", out_scores, torch.float32, (B, H, cap))
-    _need_cuda("out_positions", out_positions, torch.int32, (B, H, cap))
+    _need(i, "out_scores", out_scores, torch.float32, (B, H, cap))
+    _need(i, "out_positions", out_positions, torch.int32, (B, H, cap))
 
     def layout(t):
-        e = t.element_size()
-        return t.stride(0) * e, t.stride(1) * e, t.stride(2) * e, t.shape[3] * e
+        e, s = t.element_size(), t.stride()
+        return s[0] * e, s[1] * e, s[2] * e, t.shape[3] * e
 
     lib = load_library()
     with _On(dev, stream) as handle:
         if out_lens is None:
             out_lens = torch.empty((B,), dtype=torch.int32, device=dev)
-        _need_cuda("out_lens", out_lens, torch.int32, (B,))
+        _need(i, "out_lens", out_lens, torch.int32, (B,))
         if status is not None:
-            _need_cuda("status", status, torch.int32)
-        _one_device(dev, ("v", v), ("scores", scores), ("positions", positions), ("lens", lens), ("out_scores", out_scores),
-                    ("out_positions", out_positions), ("out_lens", out_lens), ("status", status),
-                    ("workspace_buf", workspace_buf))
+            _need(i, "status", status, torch.int32)
         ws = None
         if B > 0:
             need = _bytes("spec_evict_workspace_size", B, H, cap, int(budget))

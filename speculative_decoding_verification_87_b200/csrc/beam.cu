@@ -783,6 +783,16 @@ int launch_beam(BeamParams &p, BeamArgs &a, int dtype_index, cudaStream_t st)
 
 using namespace sv;
 
+namespace {
+struct Exp2Table {
+    double at[kExp2Tab];
+    Exp2Table()
+    {
+        for (int j = 0; j < kExp2Tab; ++j) at[j] = std::exp2(static_cast<double>(j) / kExp2Tab);
+    }
+};
+}  // namespace
+
 extern "C" size_t spec_beam_workspace_size(int batch, int beams, int vocab)
 {
     return beam_bytes(batch, beams, vocab);
@@ -837,7 +847,8 @@ extern "C" int spec_beam_select(const void *logits, spec_dtype_t dtype, int64_t 
     p.status = status;
     p.a_claim = static_cast<unsigned *>(workspace);
     p.rowpart = reinterpret_cast<float2 *>(static_cast<char *>(workspace) + kBeamAlign);
-    for (int j = 0; j < kExp2Tab; ++j) p.exp2tab[j] = std::exp2(static_cast<double>(j) / kExp2Tab);
+    static const Exp2Table table;  // 2 us of a call that takes 15
+    std::memcpy(p.exp2tab, table.at, sizeof p.exp2tab);
     BeamArgs a{end_token, keep, 0, out_scores, out_parents, out_tokens, out_finished};
     return dtype == SPEC_BF16 ? launch_beam<Bf16>(p, a, 1, stream) : launch_beam<F32>(p, a, 0, stream);
 }

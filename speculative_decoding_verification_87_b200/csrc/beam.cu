@@ -394,6 +394,9 @@ __global__ void __launch_bounds__(kBeamThreads)
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     int kind = kRowNone;  // of row tid
     if (tid == 0) bad = 0;
+    // the rehearsal may rank candidates of NaN scores, which leaves places of
+    // `best` unwritten: its beams index shared memory
+    if (tid < SPEC_MAX_BEAMS) best[tid] = {-INFINITY, 0, 0};
     if (tid < W) {
         const float sc = __ldg(p.beam_scores + static_cast<int64_t>(b) * W + tid);
         const bool done = p.beam_done && __ldg(p.beam_done + static_cast<int64_t>(b) * W + tid) != 0;

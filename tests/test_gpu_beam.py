@@ -187,6 +187,19 @@ def test_finished_beams(sv):
     assert f is out and torch.equal(f, (t == 3).int())
 
 
+@pytest.mark.parametrize("value", [float("nan"), float("inf")])
+@pytest.mark.parametrize("ended", [1, 2, 4])
+def test_ended_beams_with_bad_scores(sv, value, ended):
+    # candidates that no order ranks: more of them than one
+    x, s = rows(19, 3, 4, 1200, torch.bfloat16)
+    fin = torch.zeros((3, 4), dtype=torch.int32)
+    fin[:, :ended] = 1
+    s[1, :ended] = value
+    s[1, 0] = 0.25 if ended == 4 else value
+    _, p, _ = check(sv, x, s, 1200, 6, 1.0, fin, 11)
+    assert np.all(p[1] == -1) and np.all(p[[0, 2], 0] >= 0)
+
+
 @pytest.mark.parametrize("where", ["nan", "inf", "score nan", "score inf"])
 def test_bad_inputs_are_reported(sv, where):
     x, s = rows(9, 3, 3, 2500, torch.float32)

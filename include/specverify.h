@@ -332,6 +332,9 @@ SPECVERIFY_API int spec_plug_tokens(const int32_t *in_tokens, const int32_t *out
  * lower v.  A
  * candidate with -inf is none; slots left over get parent and token -1 and
  * score -inf.  A row of nothing but -inf has no candidate (no error).
+ * A finite score below fp32's range (a mask of the type's lowest value at
+ * T < 1, say) is a candidate, ordered by its exact value, with its parent and
+ * token, and written as -inf: the beam is out of use in the next call.
  * Outputs: out_scores [B][keep] fp32, out_parents [B][keep] (w),
  *          out_tokens [B][keep] (v), out_finished [B][keep] int32 (nullable:
  *          1 where the token is end_token, else 0).  out_scores may be

@@ -20,6 +20,7 @@
 // rows' sums in fp64 (one block, rarely: with K = 16 about one request in a
 // thousand), after which the order holds to fp64 rounding.
 #include <algorithm>
+#include <cfloat>
 #include <climits>
 #include <cmath>
 #include <cstdint>
@@ -409,9 +410,12 @@ __global__ void __launch_bounds__(kBeamThreads)
     const int items = W * S;
     const float inv_t = static_cast<float>(p.inv_t);
     auto row_of = [&](int i) { return static_cast<int>(fdiv(static_cast<unsigned>(i), p.div_s)); };
-    // score of row w's logit l (-inf: no candidate), in fp32
+    // score of row w's logit l (-inf: no candidate), in fp32.  A candidate past
+    // fp32's range (the type's lowest value as a mask, at T < 1) gets the lowest
+    // key, so that it stays one: equal keys are told apart in fp64.
     auto key_of = [&](int w, float l) -> float {
-        return rw.kind[w] != kRowLive || l == -INFINITY ? -INFINITY : fmaf(l - rw.m[w], inv_t, rw.base32[w]);
+        return rw.kind[w] != kRowLive || l == -INFINITY ? -INFINITY
+                                                        : fmaxf(fmaf(l - rw.m[w], inv_t, rw.base32[w]), -FLT_MAX);
     };
     // score of the best candidate of item i (item s of row w: w S + s)
     auto item_key = [&](int i) -> float { return key_of(row_of(i), i < kHeldItems ? held[i] : __ldcg(&part[i].x)); };
@@ -528,9 +532,10 @@ __global__ void __launch_bounds__(kBeamThreads)
             }
             __syncthreads();
             float t0f = order_value(bound);
-            if (t0f == -INFINITY && real) {
-                // fewer than K items: the K-th largest of the maxima of their
-                // parts, 32 bf16 (16 fp32) entries a lane and half
+            if (t0f <= -FLT_MAX && real) {
+                // fewer than K items (with keys above the lowest): the K-th largest
+                // of the maxima of their parts, 32 bf16 (16 fp32) entries a lane
+                // and half
                 float sub[2] = {-INFINITY, -INFINITY};
                 for (int i = warp; i < items; i += kBeamWarps) {
                     const int w = row_of(i);
@@ -551,6 +556,8 @@ __global__ void __launch_bounds__(kBeamThreads)
                 }
                 t0f = order_value(lo);
             }
+            // the lowest key stands for scores of any size: no bound
+            if (t0f <= -FLT_MAX) t0f = -INFINITY;
             // below t0 by the rows' errors, so that what the check below
             // compares is in the list too; and by the keys' rounding, at most
             // 4 steps of what adds up to a key

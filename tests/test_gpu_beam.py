@@ -269,3 +269,35 @@ def test_a_beam_search_over_several_steps(sv):
         sc, p, t = check(sv, x, scores, V, W, 1.0, fin, 9)
         fin = torch.from_numpy((t == 9).astype(np.int32))
         scores = torch.from_numpy(sc.astype(np.float32))
+
+
+def rounded(x):
+    """Exact scores as fp32 holds them: past its range, the infinity of their sign."""
+    with np.errstate(over="ignore"):
+        return np.asarray(x, np.float64).astype(np.float32).astype(np.float64)
+
+
+@pytest.mark.parametrize("dtype, W, V, K, T, at, peak", [
+    (torch.float32, 1, 5000, 6, 0.7, 2100, None), (torch.float32, 1, 1500, 64, 0.5, 1100, None),
+    (torch.float32, 3, 5000, 20, 0.3, 4800, None), (torch.bfloat16, 1, 3048, 6, 0.7, 2100, None),
+    (torch.bfloat16, 2, 3000, 12, 0.25, 2500, None), (torch.float32, 1, 128256, 8, 0.9, 127500, None),
+    (torch.float32, 2, 2000, 9, 1.0, 1500, "max"), (torch.float32, 2, 5000, 9, 1.5, 1100, None),
+])
+def test_few_allowed_beside_the_lowest_value(sv, dtype, W, V, K, T, at, peak):
+    # constrained decoding that masks with the type's lowest value: three tokens
+    # a row may be taken, the rest of the K go to masked ones in index order,
+    # although their scores lie past fp32's range (T < 1, or beside the largest)
+    x = torch.full((2, W, -(-V // 8) * 8), torch.finfo(dtype).min, dtype=dtype)
+    x[:, :, at:at + 3] = torch.tensor([1.0, 2.0, 3.0], dtype=dtype)
+    if peak:
+        x[:, :, at + 1] = torch.finfo(dtype).max
+    x[1, :, 2] = -float("inf")      # not even a masked one
+    s = torch.linspace(-1, -3, W).repeat(2, 1)
+    got, p, t, _ = sv.spec_beam_select(x.cuda(), s.cuda(), V, K, T)
+    rs, rp, rt, _, _ = ref.beam_select(x.double().numpy(), s.double().numpy(), V, K, float(np.float32(T)))
+    assert np.array_equal(p.cpu().numpy(), rp) and np.array_equal(t.cpu().numpy(), rt)
+    got, want = got.cpu().numpy().astype(np.float64), rounded(rs)
+    real = np.isfinite(want)
+    assert np.array_equal(got[~real], want[~real])
+    assert np.all(np.abs(got[real] - rs[real]) <= 6e-6 + 2.0 ** -24 * np.abs(rs[real]))
+    assert T > 1 or np.any(~real & (rp >= 0))    # some are past the range and are still candidates

@@ -328,10 +328,10 @@ SPECVERIFY_API int spec_plug_tokens(const int32_t *in_tokens, const int32_t *out
  *   scores[w] + (l[v] - m)/T - ln sum_u exp((l[u] - m)/T)   (row w; m its max).
  * The `keep` best candidates are written in order of their scores as exact
  * numbers (they are compared to within fp64 rounding; the fp32 out_scores are
- * within 6e-6 and one rounding of them), equal scores by the lower w, then the
- * lower v.  A
- * candidate with -inf is none; slots left over get parent and token -1 and
- * score -inf.  A row of nothing but -inf has no candidate (no error).
+ * within 6e-6 (7e-6 past 2^25 entries) and one rounding of them), equal scores
+ * by the lower w, then the lower v.  A candidate with -inf is none; slots left
+ * over get parent and token -1 and score -inf.  A row of nothing but -inf has no
+ * candidate (no error).
  * A finite score below fp32's range (a mask of the type's lowest value at
  * T < 1, say) is a candidate, ordered by its exact value, with its parent and
  * token, and written as -inf: the beam is out of use in the next call.

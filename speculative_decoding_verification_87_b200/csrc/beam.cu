@@ -15,7 +15,7 @@
 // request, whatever W is.
 //
 // Order.  The scores are compared as exact numbers.  Pass 1 leaves base_w
-// with an error below kBaseErr; two candidates of different rows that lie
+// with an error below kBaseErr (BeamArgs::err); two candidates of different rows that lie
 // within the sum of their rows' errors are told apart by recomputing those
 // rows' sums in fp64 (one block, rarely: with K = 16 about one request in a
 // thousand), after which the order holds to fp64 rounding.
@@ -170,16 +170,22 @@ constexpr int kListMax = 256;  // items kept on the fast path
 constexpr unsigned kRehearse = 148;   // blocks that start while pass 1 streams
 constexpr int kHeldItems = 4096;     // item maxima kept in shared memory
 constexpr int kGroups = 128;   // maxima the threshold is taken from (SPEC_MAX_BEAMS at least)
-// Bound on |ln S - ln S_exact| for a row sum merged from pass-1 partials:
-// every term carries the exponential's 2^-22 and at most |z| 2^-23 ln 2 from
-// rounding log2(e)/T and z = (l - m) log2(e)/T, whose weighted mean is at most
-// log2 V bits (entropy), 1.5e-6 for V = 2^18; the sums of an item (17
-// additions deep, 2^-24 each), the rescaling by fp32 exponentials, the sum over
-// the items and the logarithm 1.4e-6, 1.2e-6, 4e-7 and 1e-7 more.
-constexpr double kBaseErr = 6e-6;
+constexpr int kLaneItems = 4;        // a lane's items kept in registers (rows of up to 128 items)
+// Bound on |ln S - ln S_exact| for a row sum merged from pass-1 partials.  A
+// term's exponent z = (l - m) log2(e)/T comes in three parts (to the lane's, the
+// item's, the row's maximum), each with at most three roundings of half a step
+// (the difference, log2(e)/T, the product): 3 |z| 2^-24 ln 2, whose weighted
+// mean is at most log2 V bits (entropy), 3.1e-6 for V = 2^25.  The exponential
+// itself 2^-22; the sum of an item, 23 additions deep, 1.4e-6; two rescalings
+// by fp32 exponentials 6e-7; the sum over the items 5e-7 whatever their number
+// (two additions in fp32, the rest in fp64, one rounding and the warp's five); the
+// logarithm 1e-7.  Together 5.9e-6, and 6.7e-6 for the longest rows (2^31).
+constexpr double kBaseErr = 6e-6, kBaseErrLong = 7e-6;
+constexpr int kLongRow = 1 << 25;
 
 struct BeamArgs {
     int end_token, keep, cap;  // cap: candidates the shared list holds
+    double err;                // bound on the error of a row's base
     float *out_s;
     int32_t *out_p, *out_t, *out_f;
 };
@@ -452,18 +458,28 @@ __global__ void __launch_bounds__(kBeamThreads)
         for (int w = warp; w < W; w += kBeamWarps) {
             if (rw.kind[w] != kRowLive) continue;
             // the items' maxima (kept for the steps below) and the row's, then
-            // the sum of the items' sums brought to it
-            float m = -INFINITY, sum = 0.f;
-            for (int i = lane; i < S; i += 32) {
-                const float2 x = __ldcg(&part[w * S + i]);
-                if (w * S + i < kHeldItems) held[w * S + i] = x.x;
-                const float n = max_nan(m, x.x);
-                if (n == -INFINITY) continue;
-                sum = sum * ex2_approx((m - n) * p.c) + x.y * ex2_approx((x.x - n) * p.c);
-                m = n;
-            }
+            // the sum of the items' sums brought to it, each by one factor
+            float2 x[kLaneItems];
+            float m = -INFINITY;
+            auto item = [&](int i) {
+                const float2 y = __ldcg(&part[w * S + i]);
+                if (w * S + i < kHeldItems) held[w * S + i] = y.x;
+                m = max_nan(m, y.x);
+                return y;
+            };
+#pragma unroll
+            for (int j = 0; j < kLaneItems; ++j) x[j] = lane + 32 * j < S ? item(lane + 32 * j) : make_float2(-INFINITY, 0.f);
+            for (int i = lane + 32 * kLaneItems; i < S; i += 32) item(i);
             const float top = warp_max_nan(m);
-            sum = warp_sum(m == -INFINITY ? 0.f : sum * ex2_approx((m - top) * p.c));
+            auto brought = [&](float2 y) { return y.x == -INFINITY ? 0.f : y.y * ex2_approx((y.x - top) * p.c); };
+            static_assert(kLaneItems == 4, "two additions deep");
+            float sum = (brought(x[0]) + brought(x[1])) + (brought(x[2]) + brought(x[3]));
+            if (S > 32 * kLaneItems) {
+                double rest = sum;
+                for (int i = lane + 32 * kLaneItems; i < S; i += 32) rest += static_cast<double>(brought(__ldcg(&part[w * S + i])));
+                sum = static_cast<float>(rest);
+            }
+            sum = warp_sum(sum);
             if (lane == 0) {
                 rw.m[w] = top;
                 if (top == -INFINITY) {
@@ -472,7 +488,7 @@ __global__ void __launch_bounds__(kBeamThreads)
                     bad = 1;
                 } else {
                     rw.base[w] = static_cast<double>(rw.score[w]) - log_fast(sum);
-                    rw.err[w] = kBaseErr;
+                    rw.err[w] = a.err;
                     rw.base32[w] = static_cast<float>(rw.base[w]);
                 }
             }
@@ -561,7 +577,7 @@ __global__ void __launch_bounds__(kBeamThreads)
             // below t0 by the rows' errors, so that what the check below
             // compares is in the list too; and by the keys' rounding, at most
             // 4 steps of what adds up to a key
-            const double t0 = t0f == -INFINITY ? -INFINITY : static_cast<double>(t0f) - 4.0 * kBaseErr;
+            const double t0 = t0f == -INFINITY ? -INFINITY : static_cast<double>(t0f) - 4.0 * a.err;
             auto slack = [&](int w) { return 4.8e-7f * (fabsf(t0f) + fabsf(rw.base32[w])); };
             const float least = t0f == -INFINITY ? -INFINITY : static_cast<float>(t0);
             for (int i = tid; i < items; i += kBeamThreads) {
@@ -859,6 +875,6 @@ extern "C" int spec_beam_select(const void *logits, spec_dtype_t dtype, int64_t 
     p.rowpart = reinterpret_cast<float2 *>(static_cast<char *>(workspace) + kBeamAlign);
     static const Exp2Table table;  // 2 us of a call that takes 15
     std::memcpy(p.exp2tab, table.at, sizeof p.exp2tab);
-    BeamArgs a{end_token, keep, 0, out_scores, out_parents, out_tokens, out_finished};
+    BeamArgs a{end_token, keep, 0, vocab <= kLongRow ? kBaseErr : kBaseErrLong, out_scores, out_parents, out_tokens, out_finished};
     return dtype == SPEC_BF16 ? launch_beam<Bf16>(p, a, 1, stream) : launch_beam<F32>(p, a, 0, stream);
 }

@@ -301,3 +301,17 @@ def test_few_allowed_beside_the_lowest_value(sv, dtype, W, V, K, T, at, peak):
     assert np.array_equal(got[~real], want[~real])
     assert np.all(np.abs(got[real] - rs[real]) <= 6e-6 + 2.0 ** -24 * np.abs(rs[real]))
     assert T > 1 or np.any(~real & (rp >= 0))    # some are past the range and are still candidates
+
+
+@pytest.mark.parametrize("slope", [0.002 * 1.12 ** i for i in (1, 5, 7, 12, 14)])
+@pytest.mark.parametrize("V", [1 << 20, (1 << 24) - 5])
+def test_sums_of_long_rising_rows(sv, V, slope):
+    # every item's maximum is above the one before: a sum that is rescaled at
+    # each of them gathers their exponentials' errors
+    x = (torch.arange(-(-V // 4) * 4) // 1024).double().mul_(slope / 32).float()
+    s, p, t, _ = sv.spec_beam_select(x.view(1, 1, -1).cuda(), torch.zeros((1, 1), device="cuda"), V, 2)
+    y = x[:V].double()
+    best = y.max() - y.logsumexp(0)
+    first = int((x[:V] == x[V - 1]).nonzero()[0])
+    assert t.tolist() == [[first, first + 1]]
+    assert np.all(np.abs(s.cpu().double().numpy() - float(best)) <= 6e-6 + 2.0 ** -24 * abs(float(best)))

@@ -315,3 +315,18 @@ def test_sums_of_long_rising_rows(sv, V, slope):
     first = int((x[:V] == x[V - 1]).nonzero()[0])
     assert t.tolist() == [[first, first + 1]]
     assert np.all(np.abs(s.cpu().double().numpy() - float(best)) <= 6e-6 + 2.0 ** -24 * abs(float(best)))
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("B, W, K, V", [(149, 3, 5, 700), (300, 2, 4, 2100), (700, 1, 2, 90)])
+def test_more_requests_than_start_together(sv, dtype, B, W, K, V):
+    # requests whose blocks start after pass 1 has ended, ended and unused beams
+    # and bad requests among them
+    x, s = rows(B + V, B, W, V, dtype)
+    fin = torch.zeros((B, W), dtype=torch.int32)
+    fin[1::3, 0] = 1
+    s[::7, W - 1] = -float("inf")
+    x[147::10, 0, V - 1] = float("nan")
+    s[B - 2, 0] = float("nan")
+    _, p, _ = check(sv, x, s, V, K, 0.8, fin, 3)
+    assert np.all(p[B - 2] == -1) and np.any(p[148:] >= 0)

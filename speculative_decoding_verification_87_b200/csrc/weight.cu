@@ -2,11 +2,13 @@
 // give the slots of a cache, added up per key head and slot.
 //
 // Mathematics.  With s_rt = scale q_r . k_t over the rows r = (query i,
-// head g of the group), slot t gains sum_r exp(s_rt - L_r) where L_r is the
-// row's log-sum-exp over the slots it sees (t <= begin + i).  L_r needs every
-// slot of the row before the first weight can be formed.  Everything is in
-// units of log2 (scale log2 e multiplies the products), sums and statistics
-// in fp32.
+// head g of the group), slot t gains sum_r exp(s_rt - m_r) / l_r where m_r is
+// the row's maximum over the slots it sees (t <= begin + i) and l_r the sum of
+// exp(s_rt - m_r).  They need every slot of the row before the first weight can
+// be formed.  They stay two numbers: m + ln l as one would be rounded to a step
+// of its size, and every weight of the row off by as much (2.6e-6 for products
+// of 44 to 88).  Everything is in units of log2 (scale log2 e multiplies the
+// products), sums and statistics in fp32.
 //
 // Bounds: the keys' bytes while rows are few, the tensor cores and the
 // exponentials (one a row and slot in either sweep) when they are many.
@@ -62,7 +64,7 @@ struct ScoreArgs {
     int32_t *status;
     int slots;             // slots of a block (weights), of a warp's stage (statistics)
     float2 *stats;         // [B][H][R][chunks]
-    float *minus_l;        // many rows: -L [B][H][R]
+    float2 *norm;          // many rows: -m, 1 / l [B][H][R]
     int pitch;             // few rows: words between rows of products
     float *held;           // few rows: products [B][H][R][pitch]
 };
@@ -395,7 +397,7 @@ constexpr int kSumSlots = 4 * kScoreThreads;
 
 __global__ void __launch_bounds__(kScoreThreads) k_score_sum(const __grid_constant__ ScoreArgs a)
 {
-    __shared__ float L[kFewRows];
+    __shared__ float2 norm[kFewRows];  // m, 1 / l
     const int64_t head = blockIdx.y;
     const int b = static_cast<int>(head / a.H);
     const Span sp = span_of(a, b);
@@ -428,7 +430,7 @@ __global__ void __launch_bounds__(kScoreThreads) k_score_sum(const __grid_consta
             merge(mm, ll, om, ol);
             if (ol != ol) ll = ol;
         }
-        if ((threadIdx.x & 7) == 0) L[r] = mm + log2f(ll);
+        if ((threadIdx.x & 7) == 0) norm[r] = make_float2(mm, 1.f / ll);
     }
     __syncthreads();
     if (t >= sp.end) return;
@@ -440,19 +442,20 @@ __global__ void __launch_bounds__(kScoreThreads) k_score_sum(const __grid_consta
 #pragma unroll 4
         for (int r = 0; r < rows; ++r) {
             const float4 x = __ldcg(s + r * pitch);
-            const float y = L[r];
-            w[0] += ex2_approx(x.x - y);
-            w[1] += ex2_approx(x.y - y);
-            w[2] += ex2_approx(x.z - y);
-            w[3] += ex2_approx(x.w - y);
+            const float2 y = norm[r];
+            w[0] = fmaf(ex2_approx(x.x - y.x), y.y, w[0]);
+            w[1] = fmaf(ex2_approx(x.y - y.x), y.y, w[1]);
+            w[2] = fmaf(ex2_approx(x.z - y.x), y.y, w[2]);
+            w[3] = fmaf(ex2_approx(x.w - y.x), y.y, w[3]);
         }
     } else {
         for (int r = max(0, (t - sp.begin) * a.G); r < rows; ++r) {
             const float4 x = __ldcg(s + r * pitch);  // past the last slot: not used
-            const float y = L[r], z[4] = {x.x, x.y, x.z, x.w};
+            const float2 y = norm[r];
+            const float z[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-                if (r >= (t + i - sp.begin) * a.G) w[i] += ex2_approx(z[i] - y);
+                if (r >= (t + i - sp.begin) * a.G) w[i] = fmaf(ex2_approx(z[i] - y.x), y.y, w[i]);
         }
     }
 #pragma unroll
@@ -610,7 +613,7 @@ __global__ void __launch_bounds__(kScoreThreads, Many<Tag>::kBlocks) k_score_row
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
             // the scaled products are rounded here and in k_score_slots
-            // alike: fused, they would differ from L's by half a step of s
+            // alike: fused, they would differ from m's by half a step of s
             float x[8];
 #pragma unroll
             for (int n = 0; n < 4; ++n)
@@ -683,8 +686,8 @@ __global__ void __launch_bounds__(kScoreThreads, Many<Tag>::kBlocks) k_score_row
     }
 }
 
-// -L of every row from its chunks' statistics: a warp a row (6 us cold, of
-// which the launch hides all but the chain of reads).
+// -m and 1 / l of every row from its chunks' statistics: a warp a row (6 us
+// cold, of which the launch hides all but the chain of reads).
 __global__ void __launch_bounds__(kScoreThreads) k_score_merge(const __grid_constant__ ScoreArgs a)
 {
     const int lane = threadIdx.x & 31;
@@ -708,7 +711,7 @@ __global__ void __launch_bounds__(kScoreThreads) k_score_merge(const __grid_cons
         merge(m, l, om, ol);
         if (ol != ol) l = ol;
     }
-    if (lane == 0) __stcg(a.minus_l + row, -(m + log2f(l)));
+    if (lane == 0) __stcg(a.norm + row, make_float2(-m, 1.f / l));
 }
 
 // The weights of one chunk of slots: grid (chunk, request and head).
@@ -719,7 +722,7 @@ __global__ void __launch_bounds__(kScoreThreads, Many<Tag>::kBlocks) k_score_slo
     constexpr int kN = Many<Tag>::template kTiles<NB>;  // tiles of 8 slots a warp
     extern __shared__ __align__(16) unsigned char smem[];
     uint4 *sq = reinterpret_cast<uint4 *>(smem);
-    __shared__ float minus_l[kRows];
+    __shared__ float2 norm[kRows];
     const int64_t head = blockIdx.y;
     const int b = static_cast<int>(head / a.H), h = static_cast<int>(head % a.H);
     const Span sp = span_of(a, b);
@@ -742,7 +745,7 @@ __global__ void __launch_bounds__(kScoreThreads, Many<Tag>::kBlocks) k_score_slo
         if (r0 == 0) asm volatile("griddepcontrol.wait;\n" ::: "memory");
         // a row that is none weighs nothing
         for (int r = threadIdx.x; r < tiles * 16; r += kScoreThreads)
-            minus_l[r] = r < nr ? __ldcg(a.minus_l + head * a.R + r0 + r) : -INFINITY;
+            norm[r] = r < nr ? __ldcg(a.norm + head * a.R + r0 + r) : make_float2(0.f, 0.f);
         __syncthreads();
         for (int t0 = t_begin + warp * 8 * kN; t0 < t_end; t0 += kScoreWarps * 8 * kN) {
             uint4 k[kN][NB][kRaw];  // lane (g, t): elements 32 j + 8 t .. + 7 of slot g of each 8
@@ -784,21 +787,23 @@ __global__ void __launch_bounds__(kScoreThreads, Many<Tag>::kBlocks) k_score_slo
 #pragma unroll
                 for (int low = 0; low < 2; ++low) {
                     const int r = 16 * x + g + 8 * low;
-                    const float y = minus_l[r];
-                    const unsigned long long y2 = f2_pack(y, y);
+                    const float2 y = norm[r];
+                    const unsigned long long y2 = f2_pack(y.x, y.x), l2 = f2_pack(y.y, y.y);
 #pragma unroll
                     for (int n = 0; n < kN; ++n) {
                         unsigned long long z =
                             f2_add(f2_pack(__fmul_rn(c[n][2 * low], sc), __fmul_rn(c[n][2 * low + 1], sc)), y2);
-                        if (!whole) {  // the first row that sees a slot
-                            float z0, z1;
+                        unsigned long long f2 = l2;
+                        if (!whole) {  // the first row that sees a slot; others neither weigh nor pass on a NaN
+                            float z0, z1, l0 = y.y, l1 = y.y;
                             f2_unpack(z, z0, z1);
                             const int first = (t0 + 8 * n + 2 * t - sp.begin) * a.G - r0;
-                            if (r < first) z0 = -INFINITY;
-                            if (r < first + a.G) z1 = -INFINITY;
+                            if (r < first) z0 = -INFINITY, l0 = 0.f;
+                            if (r < first + a.G) z1 = -INFINITY, l1 = 0.f;
                             z = f2_pack(z0, z1);
+                            f2 = f2_pack(l0, l1);
                         }
-                        sum[n] = f2_add(sum[n], f2_ex2(z));
+                        sum[n] = f2_fma(f2_ex2(z), f2, sum[n]);
                     }
                 }
             };
@@ -920,7 +925,7 @@ int launch_few(const ScoreArgs &a, int dtype_index, cudaStream_t st)
 // step: about two blocks a SM for each, in whole stages.
 struct ManyPlan {
     int part, chunks, slots;
-    size_t stats_bytes, l_bytes;
+    size_t stats_bytes, norm_bytes;
 };
 template <class Tag>
 ManyPlan many_plan(int B, int H, int R, int C)
@@ -934,7 +939,7 @@ ManyPlan many_plan(int B, int H, int R, int C)
     const int64_t blocks = std::max<int64_t>(1, kWave / heads);
     p.slots = static_cast<int>(ceil_div(ceil_div(C, blocks), 256) * 256);
     p.stats_bytes = align_up(sizeof(float2) * static_cast<size_t>(heads) * R * p.chunks);
-    p.l_bytes = align_up(sizeof(float) * static_cast<size_t>(heads) * R);
+    p.norm_bytes = align_up(sizeof(float2) * static_cast<size_t>(heads) * R);
     return p;
 }
 
@@ -1012,7 +1017,7 @@ int launch_many(ScoreArgs a, void *workspace, int dtype_index, cudaStream_t st)
     a.part = p.part;
     a.chunks = p.chunks;
     a.slots = p.slots;
-    a.minus_l = reinterpret_cast<float *>(static_cast<char *>(workspace) + p.stats_bytes);
+    a.norm = reinterpret_cast<float2 *>(static_cast<char *>(workspace) + p.stats_bytes);
     if (a.D <= 64) return launch_many<Tag, 2>(a, dtype_index, 0, st);
     if (a.D <= 128) return launch_many<Tag, 4>(a, dtype_index, 1, st);
     return launch_many<Tag, 8>(a, dtype_index, 2, st);
@@ -1037,7 +1042,7 @@ extern "C" size_t spec_score_workspace_size(int batch, int queries, int q_heads,
         n = std::max(n, p.stats_bytes + p.held_bytes);
     }
     const ManyPlan p = many_plan<Bf16>(B, kv_heads, R, capacity), f = many_plan<F32>(B, kv_heads, R, capacity);
-    return std::max({n, p.stats_bytes + p.l_bytes, f.stats_bytes + f.l_bytes});
+    return std::max({n, p.stats_bytes + p.norm_bytes, f.stats_bytes + f.norm_bytes});
 }
 
 extern "C" int spec_cache_score(const void *q, const void *k, spec_dtype_t dtype, int64_t q_request_stride,

@@ -31,6 +31,7 @@
 // A slot's weights are summed by one thread in row order and the parts are
 // merged in a fixed order, so results do not depend on the schedule.
 #include <algorithm>
+#include <cfloat>
 #include <climits>
 #include <cmath>
 #include <cstdint>
@@ -83,7 +84,18 @@ __device__ __forceinline__ Span span_of(const ScoreArgs &a, int b)
     return s;
 }
 
-// Merge (m, l) pairs, l relative to 2^m; an empty pair is (-inf, 0).
+// (m, 1 / l) of a row as its weights take them.  A row whose products are all
+// -inf weighs nothing anywhere: (0, 0); l is at least 1 otherwise, or NaN.
+__device__ __forceinline__ float2 norm_of(float m, float l)
+{
+    return l == 0.f ? make_float2(0.f, 0.f) : make_float2(m, 1.f / l);
+}
+
+// Where a running maximum starts: below it there is only -inf, which then
+// weighs 2^-inf without a case of its own.
+constexpr float kNoMax = -FLT_MAX;
+
+// Merge (m, l) pairs, l relative to 2^m; an empty pair is (-inf or kNoMax, 0).
 __device__ __forceinline__ void merge(float &m, float &l, float om, float ol)
 {
     const float n = max_nan(m, om);
@@ -205,9 +217,10 @@ struct Slots {
     }
 };
 
-// Rows [r0, r0 + 16 * tiles) of head h below `rows` (the rest as zeros) as A
-// fragments: 1024 bytes per (16 rows, 32 elements, part), 512 a k-step, a
-// lane's 16 bytes in place.
+// Rows [r0, r0 + 16 * tiles) of head h below `rows` as A fragments: 1024 bytes
+// per (16 rows, 32 elements, part), 512 a k-step, a lane's 16 bytes in place.
+// Past `rows` the last row comes again: zeros would make NaN of an infinite
+// key, where the last row, which sees every slot, makes what its weights show.
 template <class Tag>
 __device__ __forceinline__ void stage_rows(const ScoreArgs &a, int b, int h, int r0, int rows, int tiles, int nb, uint4 *sq)
 {
@@ -221,10 +234,10 @@ __device__ __forceinline__ void stage_rows(const ScoreArgs &a, int b, int h, int
             const int i = i0 + x * threads, lane = i & 31, j = (i >> 5) % nb, tile = (i >> 5) / nb;
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
-                const int r = r0 + tile * 16 + (lane >> 2) + 8 * half, q = r / a.G, g = r - q * a.G;
+                const int r = min(r0 + tile * 16 + (lane >> 2) + 8 * half, rows - 1), q = r / a.G, g = r - q * a.G;
                 const auto *row = static_cast<const typename Tag::elem *>(a.q) + b * a.q_req + q * a.q_tok +
                                   (static_cast<int64_t>(h) * a.G + g) * a.q_head;
-                load8<Tag>(row, tile < tiles && r < rows ? 32 * j + 8 * (lane & 3) : a.D, a.D, raw[x][half]);
+                load8<Tag>(row, tile < tiles ? 32 * j + 8 * (lane & 3) : a.D, a.D, raw[x][half]);
             }
         }
 #pragma unroll
@@ -326,7 +339,7 @@ __global__ void __launch_bounds__(kScoreThreads, 2) k_score_few(const __grid_con
     __syncthreads();
     float m[MT][2], l[MT][2];
 #pragma unroll
-    for (int i = 0; i < MT; ++i) m[i][0] = m[i][1] = -INFINITY, l[i][0] = l[i][1] = 0.f;
+    for (int i = 0; i < MT; ++i) m[i][0] = m[i][1] = kNoMax, l[i][0] = l[i][1] = 0.f;
     for (; t0 < t_end; t0 += kScoreWarps * 16) {
         if (t0 + kScoreWarps * 16 < t_end) next.load(a, keys, t0 + kScoreWarps * 16, t_end);
         float c[MT][2][4];
@@ -359,7 +372,7 @@ __global__ void __launch_bounds__(kScoreThreads, 2) k_score_few(const __grid_con
                         l[i][low] *= ex2_approx(m[i][low] - top);
                         m[i][low] = top;
                     }
-                    const float mm = m[i][low] == -INFINITY ? 0.f : m[i][low];
+                    const float mm = m[i][low];
                     l[i][low] += (ex2_approx(x[0] - mm) + ex2_approx(x[1] - mm)) + (ex2_approx(x[2] - mm) + ex2_approx(x[3] - mm));
                 }
             }
@@ -430,7 +443,7 @@ __global__ void __launch_bounds__(kScoreThreads) k_score_sum(const __grid_consta
             merge(mm, ll, om, ol);
             if (ol != ol) ll = ol;
         }
-        if ((threadIdx.x & 7) == 0) norm[r] = make_float2(mm, 1.f / ll);
+        if ((threadIdx.x & 7) == 0) norm[r] = norm_of(mm, ll);
     }
     __syncthreads();
     if (t >= sp.end) return;
@@ -586,7 +599,7 @@ __global__ void __launch_bounds__(kScoreThreads, Many<Tag>::kBlocks) k_score_row
         if (s < stages) copy_slots<Tag, NB>(a, keys, t_begin + s * stage_slots, stage_slots, t_end, ring + s * stage);
         asm volatile("cp.async.commit_group;\n" ::: "memory");
     }
-    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};  // of this lane's columns, m in units of log2
+    float m[2] = {kNoMax, kNoMax}, l[2] = {0.f, 0.f};  // of this lane's columns, m in units of log2
     const float sc = a.scale2;
 
     // 32 slots from t0 on, as fragments at `tile`; `whole`: seen by every row
@@ -632,8 +645,7 @@ __global__ void __launch_bounds__(kScoreThreads, Many<Tag>::kBlocks) k_score_row
                 l[half] *= ex2_approx(m[half] - top);
                 m[half] = top;
             }
-            const float mm = !whole && m[half] == -INFINITY ? 0.f : m[half];
-            const unsigned long long nm = f2_pack(-mm, -mm);
+            const unsigned long long nm = f2_pack(-m[half], -m[half]);
             unsigned long long e01 = f2_ex2(f2_add(f2_pack(x[0], x[1]), nm));
 #pragma unroll
             for (int n = 1; n < 4; ++n) e01 = f2_add(e01, f2_ex2(f2_add(f2_pack(x[2 * n], x[2 * n + 1]), nm)));
@@ -711,7 +723,8 @@ __global__ void __launch_bounds__(kScoreThreads) k_score_merge(const __grid_cons
         merge(m, l, om, ol);
         if (ol != ol) l = ol;
     }
-    if (lane == 0) __stcg(a.norm + row, make_float2(-m, 1.f / l));
+    const float2 norm = norm_of(m, l);
+    if (lane == 0) __stcg(a.norm + row, make_float2(-norm.x, norm.y));
 }
 
 // The weights of one chunk of slots: grid (chunk, request and head).
@@ -744,8 +757,10 @@ __global__ void __launch_bounds__(kScoreThreads, Many<Tag>::kBlocks) k_score_slo
         stage_rows<Tag>(a, b, h, r0, rows, tiles, NB, sq);
         if (r0 == 0) asm volatile("griddepcontrol.wait;\n" ::: "memory");
         // a row that is none weighs nothing
-        for (int r = threadIdx.x; r < tiles * 16; r += kScoreThreads)
-            norm[r] = r < nr ? __ldcg(a.norm + head * a.R + r0 + r) : make_float2(0.f, 0.f);
+        for (int r = threadIdx.x; r < tiles * 16; r += kScoreThreads) {
+            norm[r] = __ldcg(a.norm + head * a.R + r0 + min(r, nr - 1));
+            if (r >= nr) norm[r].y = 0.f;
+        }
         __syncthreads();
         for (int t0 = t_begin + warp * 8 * kN; t0 < t_end; t0 += kScoreWarps * 8 * kN) {
             uint4 k[kN][NB][kRaw];  // lane (g, t): elements 32 j + 8 t .. + 7 of slot g of each 8

@@ -38,3 +38,65 @@ def test_equal_products_share_evenly(sv, dtype, Q, G, a):
     for i in range(Q):
         want[:n - Q + i + 1] += G / (n - Q + i + 1)
     assert np.all(np.abs(out.cpu().numpy()[0, 0] - want) <= (Q * G + 4) * 2.0 ** -24 * want)
+
+
+# ------------------------------------------------------------- infinities
+def weights(q, k, begin, end, scores, scale):
+    """state_ref.cache_score for products that may be -inf: such a slot weighs
+    nothing, and a query with no other product adds nothing.  NaN and +inf: NaN."""
+    B, H, C, D = k.shape
+    G = q.shape[2] // H
+    out, bound = scores.copy(), np.zeros_like(scores)
+    with np.errstate(invalid="ignore", over="ignore"):
+        for b in range(B):
+            b0, b1 = int(begin[b]), int(end[b])
+            out[b, :, b0:b1] = 0.0
+            for h in range(H):
+                for i in range(b1 - b0):
+                    n = b0 + i + 1
+                    for g in range(G):
+                        row, kk = q[b, i, h * G + g], k[b, h, :n]
+                        s = scale * (kk @ row)
+                        e = (D + 8) * UNIT * abs(scale) * (np.abs(kk) @ np.abs(row))
+                        m = s.max()
+                        if np.isnan(m) or m == np.inf:
+                            out[b, h, :n] = np.nan
+                            continue
+                        w = np.exp(s - m) if m > -np.inf else np.zeros(n)
+                        w /= max(w.sum(), 1e-300)
+                        out[b, h, :n] += w
+                        near = s > m - 200  # the others weigh less than 1e-80, whatever their products' rounding
+                        bound[b, h, :n] += w * np.expm1(2 * e[near].max(initial=0.0) + 2.0 ** -18)
+            bound[b, :, :b1] += ((b1 - b0) * G + 2) * 2.0 ** -24 * np.abs(np.nan_to_num(out[b, :, :b1])) + 1e-37
+    return out, bound
+
+
+def against_weights(sv, q, k, begin, end, scores, scale):
+    got = sv.spec_cache_score(q.cuda(), k.cuda(), ints(begin), ints(end), scores.cuda(), scale).cpu().numpy()
+    want, bound = weights(q.double().numpy(), k.double().numpy(), begin, end, scores.double().numpy(), scale)
+    assert np.array_equal(np.isnan(got), np.isnan(want))
+    real = ~np.isnan(want)
+    assert np.all(np.abs(got - want)[real] <= bound[real])
+    return got
+
+
+# rows of a key head: 4 and 16 (the stored form for bf16 and fp32), 18 and 72 (the sweeps, with rows left over in a tile of 16), 64
+SHAPES = [(1, 4), (4, 4), (9, 2), (9, 8), (16, 4), (33, 5)]
+INF = float("inf")
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [torch.bfloat16])
+@pytest.mark.parametrize("Q, G", SHAPES)
+def test_products_of_minus_infinity_weigh_nothing(sv, dtype, Q, G):
+    q, k, s = make(Q + G, 3, Q, G, 2, 64, 150, dtype)
+    q[..., 7] = q[..., 7].abs() + 0.25
+    k[0, :, 20:90:3, 7] = -INF          # some slots
+    k[1, 0, :, 7] = -INF                # every slot of a head: its queries add nothing
+    k[1, 1, 64:, 7] = -INF              # the last tiles of a head
+    k[2, 0, :60, 7] = -INF              # the first ones, and the step's own slots
+    k[2, 1, 150 - Q:, 7] = -INF
+    begin, end = [150 - Q, 149 - Q, 150 - Q], [150, 149, 150]
+    got = against_weights(sv, q, k, begin, end, s, 0.125)
+    assert np.all(got[0, :, 20:90:3] == s.numpy()[0, :, 20:90:3])
+    assert np.array_equal(got[1, 0, :149 - Q], s.numpy()[1, 0, :149 - Q]) and np.all(got[1, 0, 149 - Q:149] == 0)

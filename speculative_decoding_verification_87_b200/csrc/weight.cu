@@ -257,6 +257,69 @@ __device__ __forceinline__ void stage_rows(const ScoreArgs &a, int b, int h, int
     }
 }
 
+// ------------------------------------------------- fp32 numbers past bf16's range
+// The parts of an fp32 number that is infinite, or above bf16's largest, are
+// infinities of both signs, so its products come out as NaN; and so do sums
+// that pass fp32's range in one part before another.  A row's statistics and
+// a slot's weights are NaN then, and are formed once more from products in
+// plain fp32: a number where there is one, and NaN if it stays.  (One check a
+// row and chunk and one a slot: checking every product cost the sweeps 10 %.
+// bf16 products are what they are.)
+template <class Tag>
+constexpr bool kSplit = (Parts<Tag>::kParts > 1);
+
+// Row `row` (a query and head of the group) times slot `slot`, in units of log2.
+template <class Tag>
+__device__ __forceinline__ float plain_product(const ScoreArgs &a, int b, int h, int row, int slot)
+{
+    const int n = row / a.G;
+    const auto *q = static_cast<const typename Tag::elem *>(a.q) + b * a.q_req + n * a.q_tok +
+                    (static_cast<int64_t>(h) * a.G + row - n * a.G) * a.q_head;
+    const auto *k = static_cast<const typename Tag::elem *>(a.k) + b * a.k_req + h * a.k_head + slot * a.k_slot;
+    float sum = 0.f;
+#pragma unroll 4
+    for (int d = 0; d < a.D; ++d) sum = fmaf(__ldg(q + d), __ldg(k + d), sum);
+    return __fmul_rn(sum, a.scale2);
+}
+
+// (max, sum) of a row over slots [t0, t1), one warp.  `held`: the row's stored
+// products, of which those that are NaN are formed and stored again.
+template <class Tag>
+__device__ __noinline__ float2 plain_row(const ScoreArgs &a, int b, int h, int row, int t0, int t1, float *held)
+{
+    float m = kNoMax, l = 0.f;
+#pragma unroll 1
+    for (int t = t0 + static_cast<int>(threadIdx.x & 31); t < t1; t += 32) {
+        float x = held ? held[t] : NAN;
+        if (x != x) {
+            x = plain_product<Tag>(a, b, h, row, t);
+            if (held) held[t] = x;
+        }
+        if (x > m) {
+            l *= ex2_approx(m - x);
+            m = x;
+        }
+        l += ex2_approx(x - m);
+    }
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const float om = __shfl_xor_sync(kFull, m, o), ol = __shfl_xor_sync(kFull, l, o);
+        merge(m, l, om, ol);
+    }
+    return make_float2(m, l);
+}
+
+// What rows [r0, r0 + nr) give a slot, from row `first` on; `norm` as k_score_slots holds it.
+template <class Tag>
+__device__ __noinline__ float plain_slot(const ScoreArgs &a, int b, int h, int r0, int first, int nr, int slot, const float2 *norm)
+{
+    float sum = 0.f;
+#pragma unroll 1
+    for (int r = first; r < nr; ++r)
+        sum = fmaf(ex2_approx(plain_product<Tag>(a, b, h, r0 + r, slot) + norm[r].x), norm[r].y, sum);
+    return sum;
+}
+
 // The products of a warp's 16 slots with the 16-row tiles [tile0, tile0 + MT):
 // c[i][half] holds slots 8 half + 2 t, + 1 of rows g ([0], [1]) and g + 8.
 template <class Tag, int NB, int MT>
@@ -392,14 +455,26 @@ __global__ void __launch_bounds__(kScoreThreads, 2) k_score_few(const __grid_con
             if (t2 == 0) stat[warp][16 * i + g + 8 * low] = make_float2(mm, ll);
         }
     __syncthreads();
-    if (threadIdx.x < rows) {
+    const int r = threadIdx.x;
+    bool again = false;
+    if (r < rows) {
         float mm = -INFINITY, ll = 0.f;
         for (int w = 0; w < kScoreWarps; ++w) {
-            const float2 y = stat[w][threadIdx.x];
+            const float2 y = stat[w][r];
             merge(mm, ll, y.x, y.y);
             if (y.y != y.y) ll = y.y;
         }
-        __stcg(a.stats + (head * a.R + threadIdx.x) * a.chunks + blockIdx.x, make_float2(mm, ll));
+        again = ll != ll;
+        __stcg(a.stats + (head * a.R + r) * a.chunks + blockIdx.x, make_float2(mm, ll));
+    }
+    if constexpr (kSplit<Tag>) {
+        if (again) stat[0][r].y = NAN;
+        if (!__syncthreads_or(again)) return;
+        for (int x = warp; x < rows; x += kScoreWarps) {
+            if (stat[0][x].y == stat[0][x].y) continue;
+            const float2 y = plain_row<Tag>(a, b, h, x, t_begin, min(t_end, sp.begin + x / a.G + 1), held + static_cast<int64_t>(x) * a.pitch);
+            if (lane == 0) __stcg(a.stats + (head * a.R + x) * a.chunks + blockIdx.x, y);
+        }
     }
 }
 
@@ -687,6 +762,7 @@ __global__ void __launch_bounds__(kScoreThreads, Many<Tag>::kBlocks) k_score_row
         if (t == 0) stat[warp][g + 8 * half] = make_float2(mm, ll);
     }
     __syncthreads();
+    bool again = false;
     for (int r = threadIdx.x; r < nr; r += blockDim.x) {
         float mm = -INFINITY, ll = 0.f;
         for (int x = 0; x < groups; ++x) {
@@ -694,7 +770,19 @@ __global__ void __launch_bounds__(kScoreThreads, Many<Tag>::kBlocks) k_score_row
             merge(mm, ll, y.x, y.y);
             if (y.y != y.y) ll = y.y;
         }
+        if (kSplit<Tag> && ll != ll) {
+            again = true;
+            stat[r / 16][r % 16].y = NAN;
+        }
         __stcg(a.stats + (head * a.R + r0 + r) * a.chunks + blockIdx.x, make_float2(mm, ll));
+    }
+    if constexpr (kSplit<Tag>) {
+        if (!__syncthreads_or(again)) return;
+        for (int x = warp; x < nr; x += blockDim.x >> 5) {
+            if (stat[x / 16][x % 16].y == stat[x / 16][x % 16].y) continue;
+            const float2 y = plain_row<Tag>(a, b, h, r0 + x, t_begin, min(t_end, sp.begin + (r0 + x) / a.G + 1), nullptr);
+            if (lane == 0) __stcg(a.stats + (head * a.R + r0 + x) * a.chunks + blockIdx.x, y);
+        }
     }
 }
 
@@ -843,7 +931,11 @@ __global__ void __launch_bounds__(kScoreThreads, Many<Tag>::kBlocks) k_score_slo
             }
 #pragma unroll
             for (int e = 0; e < 2; ++e)
-                if (g < kN && mine + e < t_end) out[mine + e] = old[e] + add[e];
+                if (g < kN && mine + e < t_end) {
+                    if (kSplit<Tag> && add[e] != add[e])
+                        add[e] = plain_slot<Tag>(a, b, h, r0, max(0, (mine + e - sp.begin) * a.G - r0), nr, mine + e, norm);
+                    out[mine + e] = old[e] + add[e];
+                }
         }
     }
 }

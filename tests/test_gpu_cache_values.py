@@ -86,7 +86,7 @@ INF = float("inf")
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("dtype", [torch.bfloat16])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
 @pytest.mark.parametrize("Q, G", SHAPES)
 def test_products_of_minus_infinity_weigh_nothing(sv, dtype, Q, G):
     q, k, s = make(Q + G, 3, Q, G, 2, 64, 150, dtype)
@@ -100,3 +100,45 @@ def test_products_of_minus_infinity_weigh_nothing(sv, dtype, Q, G):
     got = against_weights(sv, q, k, begin, end, s, 0.125)
     assert np.all(got[0, :, 20:90:3] == s.numpy()[0, :, 20:90:3])
     assert np.array_equal(got[1, 0, :149 - Q], s.numpy()[1, 0, :149 - Q]) and np.all(got[1, 0, 149 - Q:149] == 0)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("Q, G", SHAPES)
+def test_values_next_to_the_limits(sv, dtype, Q, G):
+    # the type's largest and lowest values as keys or queries, where their
+    # products are ordinary numbers, nothing, or past the range
+    low = torch.finfo(dtype).min
+    q, k, s = make(Q * G, 4, Q, G, 2, 64, 130, dtype)
+    q[:, :, :, 5] = 0.0
+    k[0, :, ::2, 5] = low               # times zero
+    k[0, :, 1::2, 5] = -low
+    q[1, :, :, 5] = 2.0 ** -125         # products of 8
+    k[1, 0, ::3, 5] = low
+    k[1, 1, 40:, 5] = -low
+    q[2, :, :, 5] = 1.0                 # a cache masked through its keys
+    k[2, 0, ::3, 5] = low
+    k[2, 0, 77, 5] = low
+    k[2, 1, :100, 5] = low
+    q[3, :, 0, 9] = -low                # and large queries
+    k[3, :, :, 9] = 2.0 ** -126
+    begin, end = [130 - Q] * 4, [130] * 4
+    against_weights(sv, q, k, begin, end, s, 0.125)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("Q, G", SHAPES)
+def test_infinite_products(sv, dtype, Q, G):
+    # +inf and 0 * inf give NaN to the slots that the query sees, -inf none
+    q, k, s = make(Q * G, 3, Q, G, 2, 64, 130, dtype)
+    q[..., 4] = q[..., 4].abs() + 0.25
+    q[1, Q - 1, 0, 4] *= -1             # head 0: the last query's products are +inf
+    k[:2, :, 50, 4] = -INF
+    q[2, 0, 2 * G - 1, 4] = 0.0         # head 1: 0 * inf in the first query
+    k[2, 1, 129 - Q, 4] = INF
+    q[2, :, :G, 4] = -INF               # head 0: the queries' own infinities
+    k[2, 0, :, 4] = k[2, 0, :, 4].abs() + 0.25
+    begin, end = [130 - Q] * 3, [130] * 3
+    got = against_weights(sv, q, k, begin, end, s, 0.125)
+    assert np.isfinite(got[0]).all() and np.isnan(got[1, 0]).all() and np.isfinite(got[1, 1]).all()

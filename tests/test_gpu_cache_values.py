@@ -142,3 +142,102 @@ def test_infinite_products(sv, dtype, Q, G):
     begin, end = [130 - Q] * 3, [130] * 3
     got = against_weights(sv, q, k, begin, end, s, 0.125)
     assert np.isfinite(got[0]).all() and np.isnan(got[1, 0]).all() and np.isfinite(got[1, 1]).all()
+
+
+# ------------------------------------------------------------- accuracy
+def parts(x, count):
+    """x as a sum of bf16 numbers, the remainder of each rounded in turn."""
+    out, rest = [], x.clone()
+    for _ in range(count):
+        p = rest.to(torch.bfloat16).float()
+        out.append(p.double())
+        rest = rest - p
+    return out
+
+
+SIX = ((2, 0), (1, 1), (0, 2), (1, 0), (0, 1), (0, 0))
+
+
+def products(q, k, pairs, step=None):
+    """Products of fp32 rows by parts, in 64 bits; with `step`, summed up `step`
+    elements of a pair at a time in a 24-bit accumulator that truncates."""
+    p, r = parts(q, 3), parts(k, 3)
+    if step is None:
+        return sum(p[a] @ r[b].T for a, b in pairs)
+    acc = torch.zeros((q.shape[0], k.shape[0]), dtype=torch.float64)
+    for d in range(0, q.shape[1], step):
+        for a, b in pairs:
+            acc += p[a][:, d:d + step] @ r[b][:, d:d + step].T
+            m, e = torch.frexp(acc)
+            acc = torch.ldexp(torch.trunc(m * 2.0 ** 24) * 2.0 ** -24, e)
+    return acc
+
+
+def summed(s):
+    return s.softmax(1).sum(0)
+
+
+def error(x, exact):
+    return float((x - exact).norm() / exact.norm())
+
+
+# (D, rows, slots, scale): one query of all rows, so that every row sees every slot
+F32_CASES = [(64, 8, 3000, 0.125), (64, 32, 700, 1.0), (64, 40, 700, 1.0), (32, 12, 2000, 0.25)]
+
+
+def f32_case(D, R, n, scale):
+    g = torch.Generator().manual_seed(D + R)
+    q, k = torch.randn((R, D), generator=g), torch.randn((n, D), generator=g)
+    exact = summed(q.double() @ k.double().T * scale)
+    # half of what two parts a number (four products) are off
+    limit = 0.5 * error(summed(products(q, k, SIX[1:2] + SIX[3:]) * scale), exact)
+    return q, k, exact, limit
+
+
+@pytest.mark.parametrize("D, R, n, scale", F32_CASES)
+def test_the_f32_limit_tells_the_forms_apart(D, R, n, scale):
+    # six products stay within it even in an accumulator that truncates; the three
+    # largest alone do not
+    q, k, exact, limit = f32_case(D, R, n, scale)
+    assert error(summed(products(q, k, SIX, 16) * scale), exact) < limit
+    assert error(summed(products(q, k, SIX[3:]) * scale), exact) > 2 * limit
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("D, R, n, scale", F32_CASES)
+def test_f32_accuracy(sv, D, R, n, scale):
+    q, k, exact, limit = f32_case(D, R, n, scale)
+    out = sv.spec_cache_score(q.view(1, 1, R, D).cuda(), k.view(1, 1, n, D).cuda(), ints([n - 1]), ints([n]),
+                              torch.zeros((1, 1, n), device="cuda"), scale)
+    assert error(out.cpu().double()[0, 0], exact) <= limit
+
+
+def peaked(R, n):
+    """bf16 keys that lean on the first query, as real ones do: a few slots carry the weight."""
+    g = torch.Generator().manual_seed(R)
+    q = torch.randn((R, 128), generator=g).to(torch.bfloat16)
+    k = torch.randn((n, 128), generator=g) + 0.5 * torch.randn((n, 1), generator=g) * q[:1].float()
+    k = k.to(torch.bfloat16)
+    return q, k, summed(q.double() @ k.double().T * 128 ** -0.5)
+
+
+# Products of 128 bf16 terms that are summed 16 at a time with truncation come
+# out 4e-7 off (below), the exponentials (2^-22 each, of changing sign) 1e-7;
+# accumulators that keep fewer bits of each step were 6e-6 off.
+PEAKED_LIMIT = 1e-6
+
+
+@pytest.mark.parametrize("R, n", [(8, 4000), (128, 4000)])
+def test_the_peaked_limit(R, n):
+    q, k, exact = peaked(R, n)
+    s = products(q.float(), k.float(), SIX[5:], 16) * 128 ** -0.5
+    assert error(summed(s), exact) < 0.5 * PEAKED_LIMIT
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("R, n", [(8, 4000), (128, 4000)])
+def test_peaked_accuracy(sv, R, n):
+    q, k, exact = peaked(R, n)
+    out = sv.spec_cache_score(q.view(1, 1, R, 128).cuda(), k.view(1, 1, n, 128).cuda(), ints([n - 1]), ints([n]),
+                              torch.zeros((1, 1, n), device="cuda"))
+    assert error(out.cpu().double()[0, 0], exact) <= PEAKED_LIMIT

@@ -432,10 +432,17 @@ SPECVERIFY_API int spec_commit_path(void *const *states, int num_states, int64_t
  * nothing, and a query that has no other adds nothing.  8 <= D <= SPEC_MAX_HEAD_DIM, a multiple of
  * 16 bytes; Q * G and B * kv_heads at most 65535, capacity at most 2^30;
  * scale * log2(e) finite in fp32.
- * workspace: at least spec_score_workspace_size(...) bytes, 256-byte aligned,
- * not shared by calls that may overlap.
+ * workspace: at least spec_score_workspace_size_for(...) bytes of the call's
+ * type and head dimension, 256-byte aligned, not shared by calls that may
+ * overlap.  While a key head's rows Q * G are few (up to 32, and to a fraction
+ * of D) it holds their products, 4 Q G bytes a slot of the capacity and head,
+ * of as many heads at a time as fit 256 MiB; else 8 bytes a row, head and
+ * chunk of slots.  spec_score_workspace_size is enough for any type and D.
  */
 #define SPEC_MAX_HEAD_DIM 256
+SPECVERIFY_API size_t spec_score_workspace_size_for(spec_dtype_t dtype, int head_dim, int batch,
+                                                    int queries, int q_heads, int kv_heads,
+                                                    int capacity);
 SPECVERIFY_API size_t spec_score_workspace_size(int batch, int queries, int q_heads, int kv_heads,
                                                 int capacity);
 SPECVERIFY_API int spec_cache_score(const void *q, const void *k, spec_dtype_t dtype,

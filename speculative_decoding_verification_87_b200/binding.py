@@ -31,8 +31,8 @@ SYMBOLS = ("spec_verify_workspace_size", "spec_verify_strerror", "spec_verify_li
            "spec_shard_row_stats", "spec_shard_decide", "spec_shard_decide_greedy",
            "spec_shard_draw_sums", "spec_shard_draw_pick", "spec_shard_emit",
            "spec_beam_workspace_size", "spec_beam_select", "spec_reorder_beams",
-           "spec_commit_path", "spec_score_workspace_size", "spec_cache_score",
-           "spec_evict_workspace_size", "spec_cache_evict")
+           "spec_commit_path", "spec_score_workspace_size", "spec_score_workspace_size_for",
+           "spec_cache_score", "spec_evict_workspace_size", "spec_cache_evict")
 NOALLOC_SCRATCH_BYTES = 8 << 20
 
 _lib = None
@@ -116,6 +116,8 @@ def load_library(path: str = LIB_PATH):
         L.spec_commit_path.restype = _I
         L.spec_score_workspace_size.argtypes = [_I, _I, _I, _I, _I]
         L.spec_score_workspace_size.restype = _SZ
+        L.spec_score_workspace_size_for.argtypes = [_I, _I, _I, _I, _I, _I, _I]
+        L.spec_score_workspace_size_for.restype = _SZ
         L.spec_cache_score.argtypes = [_P, _P, _I, _I64, _I64, _I64, _I64, _I64, _I64, _P, _P, _I,
                                        _I, _I, _I, _I, _I, _F, _P, _P, _P, _P, _SZ, _P]
         L.spec_cache_score.restype = _I
@@ -734,13 +736,14 @@ def spec_cache_score(q, k, begin, end, scores, scale=None, out_scores=None, stat
         _need(i, "status", status, torch.int32)
     scale = D ** -0.5 if scale is None else float(scale)
     lib = load_library()
+    code = _dtype_code(q)
     with _On(dev, stream) as handle:
         ws = None
         if B > 0:
-            need = _bytes("spec_score_workspace_size", B, Q, Hq, H, cap)
+            need = _bytes("spec_score_workspace_size_for", code, D, B, Q, Hq, H, cap)
             ws = _scratch(need, workspace_buf, dev) if need else workspace_buf
         rc = lib.spec_cache_score(
-            _at(q), _at(k), _dtype_code(q), *q.stride()[:3], *k.stride()[:3], _at(begin), _at(end), B, Q, Hq, H, D, cap, scale,
+            _at(q), _at(k), code, *q.stride()[:3], *k.stride()[:3], _at(begin), _at(end), B, Q, Hq, H, D, cap, scale,
             _at(scores), _at(out_scores), _at(status), _at(ws),
             0 if ws is None else ws.numel(), handle)
     _check(rc, "spec_cache_score")

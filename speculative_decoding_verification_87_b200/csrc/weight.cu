@@ -67,7 +67,8 @@ struct ScoreArgs {
     float2 *stats;         // [B][H][R][chunks]
     float2 *norm;          // many rows: -m, 1 / l [B][H][R]
     int pitch;             // few rows: words between rows of products
-    float *held;           // few rows: products [B][H][R][pitch]
+    int head0;             // few rows: the launch's first head (of B * H)
+    float *held;           // few rows: products [heads of the launch][R][pitch]; so are stats
 };
 
 // Filled slots and queries of request b; !ok: left as it was.
@@ -375,7 +376,7 @@ __device__ __forceinline__ void products(const Slots<Tag, NB> &k, const uint4 *s
 // read takes about 36 and its start and the second kernel the rest.)
 constexpr int kFewRows = 32;
 
-// Products and statistics of one chunk of slots: grid (chunk, head).  A warp
+// Products and statistics of one chunk of slots: grid (chunk, head - head0).  A warp
 // takes every eighth 16 slots of the chunk, the next ones in flight; the
 // running (max, sum) of a row stays in the four lanes that hold it.
 template <class Tag, int NB, int MT>
@@ -384,7 +385,7 @@ __global__ void __launch_bounds__(kScoreThreads, 2) k_score_few(const __grid_con
     extern __shared__ __align__(16) unsigned char smem[];
     uint4 *sq = reinterpret_cast<uint4 *>(smem);
     __shared__ float2 stat[kScoreWarps][16 * MT];
-    const int64_t head = blockIdx.y;
+    const int64_t kept = blockIdx.y, head = a.head0 + kept;
     const int b = static_cast<int>(head / a.H), h = static_cast<int>(head % a.H);
     const Span sp = span_of(a, b);
     asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
@@ -394,7 +395,8 @@ __global__ void __launch_bounds__(kScoreThreads, 2) k_score_few(const __grid_con
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t2 = 2 * (lane & 3);
     const int nb = (a.D + 31) / 32, tiles = (rows + 15) / 16;
     const auto *keys = static_cast<const typename Tag::elem *>(a.k) + b * a.k_req + h * a.k_head;
-    float *held = a.held + head * a.R * a.pitch;
+    float *held = a.held + kept * a.R * a.pitch;
+    float2 *stats = a.stats + kept * a.R * a.chunks + blockIdx.x;
     Slots<Tag, NB> cur, next;
     int t0 = t_begin + warp * 16;
     if (t0 < t_end) cur.load(a, keys, t0, t_end);
@@ -465,7 +467,7 @@ __global__ void __launch_bounds__(kScoreThreads, 2) k_score_few(const __grid_con
             if (y.y != y.y) ll = y.y;
         }
         again = ll != ll;
-        __stcg(a.stats + (head * a.R + r) * a.chunks + blockIdx.x, make_float2(mm, ll));
+        __stcg(stats + static_cast<int64_t>(r) * a.chunks, make_float2(mm, ll));
     }
     if constexpr (kSplit<Tag>) {
         if (again) stat[0][r].y = NAN;
@@ -473,12 +475,12 @@ __global__ void __launch_bounds__(kScoreThreads, 2) k_score_few(const __grid_con
         for (int x = warp; x < rows; x += kScoreWarps) {
             if (stat[0][x].y == stat[0][x].y) continue;
             const float2 y = plain_row<Tag>(a, b, h, x, t_begin, min(t_end, sp.begin + x / a.G + 1), held + static_cast<int64_t>(x) * a.pitch);
-            if (lane == 0) __stcg(a.stats + (head * a.R + x) * a.chunks + blockIdx.x, y);
+            if (lane == 0) __stcg(stats + static_cast<int64_t>(x) * a.chunks, y);
         }
     }
 }
 
-// The weights of kSumSlots slots: grid (slots, head), four slots a thread
+// The weights of kSumSlots slots: grid (slots, head - head0), four slots a thread
 // (with one, four times as many blocks merge the statistics: 17 us of the
 // decode call's 59 under a profiler).
 constexpr int kSumSlots = 4 * kScoreThreads;
@@ -486,7 +488,7 @@ constexpr int kSumSlots = 4 * kScoreThreads;
 __global__ void __launch_bounds__(kScoreThreads) k_score_sum(const __grid_constant__ ScoreArgs a)
 {
     __shared__ float2 norm[kFewRows];  // m, 1 / l
-    const int64_t head = blockIdx.y;
+    const int64_t kept = blockIdx.y, head = a.head0 + kept;
     const int b = static_cast<int>(head / a.H);
     const Span sp = span_of(a, b);
     if (!sp.ok) {
@@ -508,7 +510,7 @@ __global__ void __launch_bounds__(kScoreThreads) k_score_sum(const __grid_consta
         float mm = -INFINITY, ll = 0.f;
         if (r < rows)
             for (int c = threadIdx.x & 7; c < chunks; c += 8) {
-                const float2 y = __ldcg(a.stats + (head * a.R + r) * a.chunks + c);
+                const float2 y = __ldcg(a.stats + (kept * a.R + r) * a.chunks + c);
                 merge(mm, ll, y.x, y.y);
                 if (y.y != y.y) ll = y.y;
             }
@@ -523,7 +525,7 @@ __global__ void __launch_bounds__(kScoreThreads) k_score_sum(const __grid_consta
     __syncthreads();
     if (t >= sp.end) return;
     // the step's weight by itself, in row order, then the old value
-    const float4 *s = reinterpret_cast<const float4 *>(a.held + head * a.R * a.pitch + t);
+    const float4 *s = reinterpret_cast<const float4 *>(a.held + kept * a.R * a.pitch + t);
     const int64_t pitch = a.pitch / 4;
     float w[4] = {0.f, 0.f, 0.f, 0.f};
     if (t + 3 <= sp.begin) {  // seen by every row
@@ -959,7 +961,15 @@ bool few_rows(bool f32, int R, int D, int64_t slots)
     return slots >= 1 << 18 ? R <= kFewRows && 4 * R <= D : R <= 16 && 8 * R <= D;
 }
 
+// What the stored products may take: the heads go in groups that fit, and the
+// next group's products overwrite the last one's.  (Two groups / one, D = 128
+// bf16: 128 heads of 262144 slots, 4 rows 1372 / 1325 us; 64 of 131072, 16 rows
+// 397 / 390; 64 of 65536, 32 rows 266 / 266.  Swept twice the keys would be read
+// once more.)
+constexpr size_t kHeldMost = size_t(256) << 20;
+
 struct FewPlan {
+    int heads;  // of a group; 0: not even one fits
     int part, chunks, pitch;
     size_t stats_bytes, held_bytes;
 };
@@ -968,20 +978,22 @@ struct FewPlan {
 FewPlan few_plan(int B, int H, int R, int C)
 {
     FewPlan p;
-    const int64_t heads = static_cast<int64_t>(B) * H;
+    const int64_t pitch = ceil_div(C, 32) * 32;
+    p.pitch = static_cast<int>(pitch);
+    const size_t one = sizeof(float) * static_cast<size_t>(R) * static_cast<size_t>(pitch);
+    p.heads = static_cast<int>(std::min<int64_t>(static_cast<int64_t>(B) * H, static_cast<int64_t>(kHeldMost / one)));
     p.part = 1024;
-    while (p.part > kPartSlots && heads * ceil_div(C, p.part) < 4 * 148) p.part /= 2;
+    while (p.part > kPartSlots && p.heads * ceil_div(C, p.part) < 4 * 148) p.part /= 2;
     p.chunks = static_cast<int>(ceil_div(C, p.part));
-    p.pitch = static_cast<int>(ceil_div(C, 32) * 32);
-    p.stats_bytes = align_up(sizeof(float2) * static_cast<size_t>(heads) * R * p.chunks);
-    p.held_bytes = align_up(sizeof(float) * static_cast<size_t>(heads) * R * p.pitch);
+    p.stats_bytes = align_up(sizeof(float2) * static_cast<size_t>(p.heads) * R * p.chunks);
+    p.held_bytes = align_up(one * p.heads);
     return p;
 }
 
 bool g_few_attr[64][2][3][2];
 
 template <class Tag, int NB, int MT>
-int launch_few(const ScoreArgs &a, int dtype_index, int nb_index, int mt_index, cudaStream_t st)
+int launch_few(ScoreArgs a, int group, int dtype_index, int nb_index, int mt_index, cudaStream_t st)
 {
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return SPEC_ECUDA;
@@ -996,36 +1008,38 @@ int launch_few(const ScoreArgs &a, int dtype_index, int nb_index, int mt_index, 
             g_few_attr[dev][dtype_index][nb_index][mt_index] = true;
         }
     }
-    const unsigned heads = static_cast<unsigned>(a.B * a.H);
-    k_score_few<Tag, NB, MT><<<dim3(static_cast<unsigned>(a.chunks), heads), kScoreThreads, smem, st>>>(a);
-    if (cudaGetLastError() != cudaSuccess) return SPEC_ECUDA;
-    cudaLaunchConfig_t cfg = {};
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.gridDim = dim3(static_cast<unsigned>(ceil_div(a.C, kSumSlots)), heads);
-    cfg.blockDim = dim3(kScoreThreads);
-    cfg.stream = st;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    if (cudaLaunchKernelEx(&cfg, k_score_sum, a) != cudaSuccess) {
-        (void)cudaGetLastError();
-        return SPEC_ECUDA;
+    for (; a.head0 < a.B * a.H; a.head0 += group) {
+        const unsigned heads = static_cast<unsigned>(std::min(group, a.B * a.H - a.head0));
+        k_score_few<Tag, NB, MT><<<dim3(static_cast<unsigned>(a.chunks), heads), kScoreThreads, smem, st>>>(a);
+        if (cudaGetLastError() != cudaSuccess) return SPEC_ECUDA;
+        cudaLaunchConfig_t cfg = {};
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[0].val.programmaticStreamSerializationAllowed = 1;
+        cfg.gridDim = dim3(static_cast<unsigned>(ceil_div(a.C, kSumSlots)), heads);
+        cfg.blockDim = dim3(kScoreThreads);
+        cfg.stream = st;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        if (cudaLaunchKernelEx(&cfg, k_score_sum, a) != cudaSuccess) {
+            (void)cudaGetLastError();
+            return SPEC_ECUDA;
+        }
     }
     return SPEC_OK;
 }
 template <class Tag, int NB>
-int launch_few(const ScoreArgs &a, int dtype_index, int nb_index, cudaStream_t st)
+int launch_few(const ScoreArgs &a, int group, int dtype_index, int nb_index, cudaStream_t st)
 {
-    return a.R <= 16 ? launch_few<Tag, NB, 1>(a, dtype_index, nb_index, 0, st)
-                     : launch_few<Tag, NB, 2>(a, dtype_index, nb_index, 1, st);
+    return a.R <= 16 ? launch_few<Tag, NB, 1>(a, group, dtype_index, nb_index, 0, st)
+                     : launch_few<Tag, NB, 2>(a, group, dtype_index, nb_index, 1, st);
 }
 template <class Tag>
-int launch_few(const ScoreArgs &a, int dtype_index, cudaStream_t st)
+int launch_few(const ScoreArgs &a, int group, int dtype_index, cudaStream_t st)
 {
-    if (a.D <= 64) return launch_few<Tag, 2>(a, dtype_index, 0, st);
-    if (a.D <= 128) return launch_few<Tag, 4>(a, dtype_index, 1, st);
-    return launch_few<Tag, 8>(a, dtype_index, 2, st);
+    if (a.D <= 64) return launch_few<Tag, 2>(a, group, dtype_index, 0, st);
+    if (a.D <= 128) return launch_few<Tag, 4>(a, group, dtype_index, 1, st);
+    return launch_few<Tag, 8>(a, group, dtype_index, 2, st);
 }
 
 // Chunks of slots of the statistics step and slots of a block of the weights
@@ -1135,21 +1149,51 @@ int launch_many(ScoreArgs a, void *workspace, int dtype_index, cudaStream_t st)
 
 using namespace sv;
 
+namespace {
+// The form of a call and what it needs.
+struct ScorePlan {
+    bool few;
+    FewPlan f;
+    size_t bytes;
+};
+ScorePlan score_plan(bool f32, int D, int B, int H, int R, int C)
+{
+    ScorePlan p;
+    p.f = few_plan(B, H, R, C);
+    p.few = p.f.heads > 0 && few_rows(f32, R, D, static_cast<int64_t>(B) * H * C);
+    if (p.few) {
+        p.bytes = p.f.stats_bytes + p.f.held_bytes;
+    } else {
+        const ManyPlan m = f32 ? many_plan<F32>(B, H, R, C) : many_plan<Bf16>(B, H, R, C);
+        p.bytes = m.stats_bytes + m.norm_bytes;
+    }
+    return p;
+}
+
+bool score_sizes(int batch, int queries, int q_heads, int kv_heads, int capacity)
+{
+    return batch >= 0 && queries >= 1 && kv_heads >= 1 && q_heads >= kv_heads && q_heads % kv_heads == 0 && capacity >= 1 &&
+           static_cast<int64_t>(queries) * (q_heads / kv_heads) <= INT_MAX;
+}
+}  // namespace
+
+extern "C" size_t spec_score_workspace_size_for(spec_dtype_t dtype, int head_dim, int batch, int queries, int q_heads,
+                                                int kv_heads, int capacity)
+{
+    if ((dtype != SPEC_F32 && dtype != SPEC_BF16) || head_dim < 1 || !score_sizes(batch, queries, q_heads, kv_heads, capacity))
+        return 0;
+    return score_plan(dtype == SPEC_F32, head_dim, std::max(batch, 1), kv_heads, queries * (q_heads / kv_heads), capacity).bytes;
+}
+
+// Whichever form a type and head dimension takes: the rules turn to stored
+// products as D grows, so the most is that of one of their ends.
 extern "C" size_t spec_score_workspace_size(int batch, int queries, int q_heads, int kv_heads, int capacity)
 {
-    if (batch < 0 || queries < 1 || kv_heads < 1 || q_heads < kv_heads || q_heads % kv_heads != 0 || capacity < 1)
-        return 0;
-    const int64_t rows = static_cast<int64_t>(queries) * (q_heads / kv_heads);
-    if (rows > INT_MAX) return 0;
-    const int B = std::max(batch, 1), R = static_cast<int>(rows);
-    // whichever form a type and head dimension takes
-    size_t n = kScoreAlign;
-    if (R <= kFewRows) {
-        const FewPlan p = few_plan(B, kv_heads, R, capacity);
-        n = std::max(n, p.stats_bytes + p.held_bytes);
-    }
-    const ManyPlan p = many_plan<Bf16>(B, kv_heads, R, capacity), f = many_plan<F32>(B, kv_heads, R, capacity);
-    return std::max({n, p.stats_bytes + p.norm_bytes, f.stats_bytes + f.norm_bytes});
+    size_t most = 0;
+    for (const spec_dtype_t dtype : {SPEC_F32, SPEC_BF16})
+        for (const int dim : {8, SPEC_MAX_HEAD_DIM})
+            most = std::max(most, spec_score_workspace_size_for(dtype, dim, batch, queries, q_heads, kv_heads, capacity));
+    return most;
 }
 
 extern "C" int spec_cache_score(const void *q, const void *k, spec_dtype_t dtype, int64_t q_request_stride,
@@ -1182,9 +1226,10 @@ extern "C" int spec_cache_score(const void *q, const void *k, spec_dtype_t dtype
     if (batch == 0) return SPEC_OK;
     if (!q || !k || !begin || !end || !scores || !out_scores) return SPEC_EINVAL;
     if (((reinterpret_cast<uintptr_t>(q) | reinterpret_cast<uintptr_t>(k)) & 15u) != 0) return SPEC_EALIGN;
-    if (!workspace || (reinterpret_cast<uintptr_t>(workspace) % kScoreAlign) != 0 || workspace_bytes < spec_score_workspace_size(batch, queries, q_heads, kv_heads, capacity))
-        return SPEC_EWORKSPACE;
     const bool f32 = dtype == SPEC_F32;
+    const ScorePlan plan = score_plan(f32, head_dim, batch, kv_heads, queries * (q_heads / kv_heads), capacity);
+    if (!workspace || (reinterpret_cast<uintptr_t>(workspace) % kScoreAlign) != 0 || workspace_bytes < plan.bytes)
+        return SPEC_EWORKSPACE;
     if (static_cast<int64_t>(batch) * kv_heads > 65535) return SPEC_EUNSUPPORTED;
     ScoreArgs a;
     std::memset(&a, 0, sizeof a);
@@ -1210,13 +1255,12 @@ extern "C" int spec_cache_score(const void *q, const void *k, spec_dtype_t dtype
     a.out = out_scores;
     a.status = status;
     a.stats = static_cast<float2 *>(workspace);
-    if (few_rows(f32, a.R, head_dim, static_cast<int64_t>(batch) * kv_heads * capacity)) {
-        const FewPlan few = few_plan(batch, kv_heads, a.R, capacity);
-        a.part = few.part;
-        a.chunks = few.chunks;
-        a.pitch = few.pitch;
-        a.held = reinterpret_cast<float *>(static_cast<char *>(workspace) + few.stats_bytes);
-        return f32 ? launch_few<F32>(a, 0, stream) : launch_few<Bf16>(a, 1, stream);
+    if (plan.few) {
+        a.part = plan.f.part;
+        a.chunks = plan.f.chunks;
+        a.pitch = plan.f.pitch;
+        a.held = reinterpret_cast<float *>(static_cast<char *>(workspace) + plan.f.stats_bytes);
+        return f32 ? launch_few<F32>(a, plan.f.heads, 0, stream) : launch_few<Bf16>(a, plan.f.heads, 1, stream);
     }
     return f32 ? launch_many<F32>(a, workspace, 0, stream) : launch_many<Bf16>(a, workspace, 1, stream);
 }

@@ -241,3 +241,52 @@ def test_peaked_accuracy(sv, R, n):
     out = sv.spec_cache_score(q.view(1, 1, R, 128).cuda(), k.view(1, 1, n, 128).cuda(), ints([n - 1]), ints([n]),
                               torch.zeros((1, 1, n), device="cuda"))
     assert error(out.cpu().double()[0, 0], exact) <= PEAKED_LIMIT
+
+
+# ------------------------------------------------------------- workspaces
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("Q, G", SHAPES + [(8, 4)])
+@pytest.mark.parametrize("D", [64, 128])
+def test_workspace_of_the_form_is_enough(sv, dtype, Q, G, D):
+    q, k, s = make(3 * Q + G, 2, Q, G, 2, D, 300, dtype)
+    begin, end = ints([300 - Q, 250 - Q]), ints([300, 250])
+    need = sv.load_library().spec_score_workspace_size_for(int(dtype == torch.bfloat16), D, 2, Q, 2 * G, 2, 300)
+    want = sv.spec_cache_score(q.cuda(), k.cuda(), begin, end, s.cuda())
+    store = torch.full((need + 1024,), 171, dtype=torch.uint8, device="cuda")
+    got = sv.spec_cache_score(q.cuda(), k.cuda(), begin, end, s.cuda(), workspace_buf=store[:need])
+    assert torch.equal(got, want) and torch.all(store[need:] == 171)
+    with pytest.raises(sv.SpecVerifyError):
+        sv.spec_cache_score(q.cuda(), k.cuda(), begin, end, s.cuda(), workspace_buf=store[:need - 1])
+
+
+@pytest.mark.gpu
+def test_heads_in_groups(sv):
+    # 32 rows of 65536 slots are 8 MiB of products a head: 40 heads go 32 and 8 at
+    # a time, a request's heads on both sides
+    B, H, C, R, D = 8, 5, 65536, 32, 128
+    g = torch.Generator(device="cuda").manual_seed(2)
+    q = torch.randn((B, 1, H * R, D), generator=g, device="cuda").to(torch.bfloat16)
+    k = torch.randn((B, H, C, D), generator=g, device="cuda").to(torch.bfloat16)
+    s = torch.rand((B, H, C), generator=g, device="cuda")
+    end = torch.tensor([C - 4099 * b for b in range(B)], dtype=torch.int32)
+    end[4] = C + 1                      # a request that is left as it was
+    status = ints([0])
+    out = sv.spec_cache_score(q, k, end.cuda() - 1, end.cuda(), s, out_scores=torch.full_like(s, -7.0), status=status)
+    assert status.item() == 16 and torch.all(out[4] == -7.0)
+    scale = D ** -0.5
+    for b in range(B):
+        n = int(end[b])
+        if n > C:
+            continue
+        assert torch.all(out[b, :, n:] == -7.0)
+        for h in range(H):
+            x, y = q[b, 0, h * R:(h + 1) * R].double(), k[b, h, :n].double()
+            w = (x @ y.T * scale).softmax(1)
+            # as state_ref.cache_score bounds it
+            e = (D + 8) * UNIT * scale * (x.abs() @ y.abs().T).amax(1, keepdim=True)
+            want = s[b, h, :n].double()
+            want[n - 1] = 0
+            want = want + w.sum(0)
+            bound = (w * torch.expm1(2 * e + 2.0 ** -18)).sum(0) + (R + 2) * 2.0 ** -24 * want
+            assert torch.all((out[b, h, :n].double() - want).abs() <= bound)

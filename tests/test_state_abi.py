@@ -243,3 +243,21 @@ def test_reference_evict_by_hand():
 def test_evict_rows_that_overlap_are_refused(lib, want, change):
     # what gets past the check stops at the workspace's
     assert _evict(lib, ws=0, **change) == (EWORKSPACE if want == OK else want)
+
+
+def test_score_workspace_of_a_type_and_head_dimension(lib):
+    size, f32, bf16 = lib.spec_score_workspace_size_for, 0, 1
+    # 32 rows of 64 elements are swept twice: their products are not stored
+    assert 0 < size(bf16, 64, 32, 8, 32, 8, 32768) < 1 << 20
+    # where they are, in groups of heads that fit 256 MiB (and the chunks' statistics)
+    most = (256 << 20) + (8 << 20)
+    assert 256 * 4 * 32768 * 4 <= size(bf16, 128, 32, 1, 32, 8, 32768) <= most
+    assert size(bf16, 128, 32, 8, 32, 8, 32768) <= most and size(bf16, 128, 64, 4, 32, 8, 1 << 20) <= most
+    # a head that does not fit by itself is swept
+    assert size(bf16, 128, 1, 32, 1, 1, 1 << 30) < 1 << 20
+    # what is enough for any of them
+    for args in ((1, 2, 2, 1, 100), (32, 8, 32, 8, 32768), (4, 1, 32, 8, 9000), (2, 40, 8, 2, 500), (1, 3, 1, 1, 64)):
+        each = [size(t, d, *args) for t in (f32, bf16) for d in range(8, 257, 8)]
+        assert lib.spec_score_workspace_size(*args) == max(each) and min(each) > 0
+    assert size(2, 64, 1, 1, 1, 1, 10) == 0 and size(bf16, 0, 1, 1, 1, 1, 10) == 0 and size(bf16, 64, 1, 1, 3, 2, 10) == 0
+    assert size(bf16, 64, 0, 1, 1, 1, 10) > 0

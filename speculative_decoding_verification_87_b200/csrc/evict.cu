@@ -576,12 +576,15 @@ int launch_evict(const EvictArgs &a, cudaStream_t stream)
     const int64_t heads = static_cast<int64_t>(a.B) * a.H;
     if (a.C <= kSmallSlots) {
         // One kernel while a block a head moves its rows as fast as the whole
-        // GPU would: few moves, or heads for most SMs (32 heads, one kernel /
-        // two: 128 moves 9.6 / 10.5 us, 256 11.9 / 10.5; 128 heads: 128 moves
-        // 10.4 / 12.0, 512 16.0 / 18.6, 2048 42 / 39; 512 heads: 2048 moves
-        // 119 / 137).  The lengths must not be overwritten while other heads
-        // read them.
-        if ((a.most <= 128 || heads >= 128) && a.out_lens != a.lens) {
+        // GPU would: few moves, or heads for most SMs.  (One kernel / two, us.  32
+        // heads: 100 moves 8.1 / 9.9, 200 9.1 / 10.1, 400 11.1 / 11.0, 650 13.5 /
+        // 12.2; 64 of 4096 slots: 400 16.9 / 14.9, 512 19.8 / 16.4; 128: 200 9.3 /
+        // 11.7, 512 14.6 / 17.2, 1024 22.8 / 20.9, 2048 37.2 / 29.9; 192: 1024 29.8 /
+        // 28.8, 2048 49.1 / 42.6; 256: 1024 31.4 / 33.3, 2048 53.3 / 52.6; 512: 2048
+        // 90.2 / 96.3.)  The lengths must not be overwritten while other heads read
+        // them.
+        const bool one = a.most <= 128 || (heads >= 128 && a.most <= 512) || heads >= 256;
+        if (one && a.out_lens != a.lens) {
             k_evict_small<T, true><<<static_cast<unsigned>(heads), kSmallThreads, 0, stream>>>(a);
             return cudaGetLastError() == cudaSuccess ? SPEC_OK : SPEC_ECUDA;
         }

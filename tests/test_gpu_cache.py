@@ -261,6 +261,15 @@ def test_evict_between_one_kernel_and_two(sv, B, H, C, budget):
     check_evict(sv, scores, pos, lens, budget, 2, 10, inplace=True)
 
 
+@pytest.mark.parametrize("B, H, C, budget", [(16, 8, 1024, 512), (16, 8, 1026, 513), (51, 5, 1400, 700), (64, 4, 1400, 700)])
+def test_evict_of_many_moves_in_one_kernel_or_two(sv, B, H, C, budget):
+    scores, pos = cache(C + budget + B, B, H, C)
+    lens = np.random.RandomState(B).randint(0, C + 1, B)
+    lens[0] = C
+    check_evict(sv, scores, pos, lens, budget, 2, 10)
+    check_evict(sv, scores, pos, lens, budget, 2, 10, inplace=True)
+
+
 @pytest.mark.parametrize("dtype, D, Dv", [(torch.float32, 1, 3), (torch.bfloat16, 5, 16), (torch.int8, 7, 1),
                                           (torch.float32, 128, 64), (torch.bfloat16, 576, 512), (torch.int8, 20, 4)])
 def test_evict_rows(sv, dtype, D, Dv):

@@ -167,7 +167,6 @@ __global__ void __launch_bounds__(kThreads, 2) k_beam_pass1(const __grid_constan
 constexpr int kBeamThreads = 512;
 constexpr int kBeamWarps = kBeamThreads / 32;
 constexpr int kListMax = 256;  // items kept on the fast path
-constexpr unsigned kRehearse = 148;   // blocks that start while pass 1 streams
 constexpr int kHeldItems = 4096;     // item maxima kept in shared memory
 constexpr int kGroups = 128;   // maxima the threshold is taken from (SPEC_MAX_BEAMS at least)
 constexpr int kLaneItems = 4;        // a lane's items kept in registers (rows of up to 128 items)
@@ -377,9 +376,10 @@ __device__ __forceinline__ double exact_sum(const Params &p, int b, int w, float
 }
 
 // Select: one block per request, after pass 1.  A chain of block-wide steps
-// bounds it, not bytes: 6 to 10 us after pass 1's end for K = 16 (19 us under a
-// profiler, which starts it cold), some 26 to 35 more where rows' sums are
-// recomputed.
+// bounds it, not bytes: 6 us after pass 1's end for one request with K = 4, 9
+// for 32 with K = 16.  Where rows' sums are recomputed each of 128256 entries
+// takes some 20 us more, one after the other: equal beams, which are all
+// recomputed, take 97 us for 4 and 1.34 ms for 64 (12 and 36 for distinct ones).
 template <class Tag>
 __global__ void __launch_bounds__(kBeamThreads)
     k_beam_select(const __grid_constant__ BeamParams p, const __grid_constant__ BeamArgs a)
@@ -399,19 +399,16 @@ __global__ void __launch_bounds__(kBeamThreads)
 
     const int b = blockIdx.x, W = p.R, S = p.S, K = a.keep;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    int kind = kRowNone;  // of row tid
     if (tid == 0) bad = 0;
-    // the rehearsal may rank candidates of NaN scores, which leaves places of
-    // `best` unwritten: its beams index shared memory
-    if (tid < SPEC_MAX_BEAMS) best[tid] = {-INFINITY, 0, 0};
+    __syncthreads();
     if (tid < W) {
         const float sc = __ldg(p.beam_scores + static_cast<int64_t>(b) * W + tid);
         const bool done = p.beam_done && __ldg(p.beam_done + static_cast<int64_t>(b) * W + tid) != 0;
-        kind = sc == -INFINITY ? kRowNone : done ? kRowDone : kRowLive;
         rw.score[tid] = sc;
-        rw.kind[tid] = kind;
+        rw.kind[tid] = sc == -INFINITY ? kRowNone : done ? kRowDone : kRowLive;
+        rw.exact[tid] = 0;
+        if (!(sc < INFINITY)) bad = 1;  // NaN or +inf
     }
-    __syncthreads();
     const float2 *part = p.rowpart + static_cast<int64_t>(b) * W * S;
     const int items = W * S;
     const float inv_t = static_cast<float>(p.inv_t);
@@ -433,289 +430,273 @@ __global__ void __launch_bounds__(kBeamThreads)
         return m == -INFINITY ? -INFINITY
                               : rw.base[w] + (static_cast<double>(m) - static_cast<double>(rw.m[w])) * p.inv_t;
     };
-    // The steps run twice: a rehearsal while pass 1 still streams, over what the
-    // workspace happens to hold, then the real one.  The kernel is a chain of
-    // short steps, each of whose instructions came from L2 in a cold launch;
-    // the rehearsal fetches them (and the translations of the rows' pages) in
-    // time that is spent waiting anyway.  It writes nothing but shared memory.
-    // (Blocks past the first wave start when pass 1 is done: they skip it.)
     const int64_t o = static_cast<int64_t>(b) * K;
     int found = 0;
-#pragma unroll 1
-    for (int run = blockIdx.x < kRehearse ? 0 : 1; run < 2; ++run) {
-        const bool real = run == 1;
-        if (real) {
-            __syncthreads();
-            if (tid < W) {
-                rw.kind[tid] = kind;
-                rw.exact[tid] = 0;
-                if (!(rw.score[tid] < INFINITY)) bad = 1;  // NaN or +inf
-            }
-            asm volatile("griddepcontrol.wait;\n" ::: "memory");
-            __syncthreads();
-        }
-        // merge the rows, a warp each
-        for (int w = warp; w < W; w += kBeamWarps) {
-            if (rw.kind[w] != kRowLive) continue;
-            // the items' maxima (kept for the steps below) and the row's, then
-            // the sum of the items' sums brought to it, each by one factor
-            float2 x[kLaneItems];
-            float m = -INFINITY;
-            auto item = [&](int i) {
-                const float2 y = __ldcg(&part[w * S + i]);
-                if (w * S + i < kHeldItems) held[w * S + i] = y.x;
-                m = max_nan(m, y.x);
-                return y;
-            };
+    // (Running the steps once on the last call's partials while pass 1 streams, to
+    // have their instructions at hand, took 2.7 us more of 8.8: blocks start when
+    // the first of pass 1 leave, so the first run is waited for too; on partials of
+    // other contents 10 us more.)
+    asm volatile("griddepcontrol.wait;\n" ::: "memory");
+    __syncthreads();
+    // merge the rows, a warp each
+    for (int w = warp; w < W; w += kBeamWarps) {
+        if (rw.kind[w] != kRowLive) continue;
+        // the items' maxima (kept for the steps below) and the row's, then
+        // the sum of the items' sums brought to it, each by one factor
+        float2 x[kLaneItems];
+        float m = -INFINITY;
+        auto item = [&](int i) {
+            const float2 y = __ldcg(&part[w * S + i]);
+            if (w * S + i < kHeldItems) held[w * S + i] = y.x;
+            m = max_nan(m, y.x);
+            return y;
+        };
 #pragma unroll
-            for (int j = 0; j < kLaneItems; ++j) x[j] = lane + 32 * j < S ? item(lane + 32 * j) : make_float2(-INFINITY, 0.f);
-            for (int i = lane + 32 * kLaneItems; i < S; i += 32) item(i);
-            const float top = warp_max_nan(m);
-            auto brought = [&](float2 y) { return y.x == -INFINITY ? 0.f : y.y * ex2_approx((y.x - top) * p.c); };
-            static_assert(kLaneItems == 4, "two additions deep");
-            float sum = (brought(x[0]) + brought(x[1])) + (brought(x[2]) + brought(x[3]));
-            if (S > 32 * kLaneItems) {
-                double rest = sum;
-                for (int i = lane + 32 * kLaneItems; i < S; i += 32) rest += static_cast<double>(brought(__ldcg(&part[w * S + i])));
-                sum = static_cast<float>(rest);
-            }
-            sum = warp_sum(sum);
-            if (lane == 0) {
-                rw.m[w] = top;
-                if (top == -INFINITY) {
-                    rw.kind[w] = kRowNone;  // nothing to go on with
-                } else if (!stoch_row_ok(top, sum)) {
-                    bad = 1;
-                } else {
-                    rw.base[w] = static_cast<double>(rw.score[w]) - log_fast(sum);
-                    rw.err[w] = a.err;
-                    rw.base32[w] = static_cast<float>(rw.base[w]);
-                }
-            }
-            __syncwarp();
+        for (int j = 0; j < kLaneItems; ++j) x[j] = lane + 32 * j < S ? item(lane + 32 * j) : make_float2(-INFINITY, 0.f);
+        for (int i = lane + 32 * kLaneItems; i < S; i += 32) item(i);
+        const float top = warp_max_nan(m);
+        auto brought = [&](float2 y) { return y.x == -INFINITY ? 0.f : y.y * ex2_approx((y.x - top) * p.c); };
+        static_assert(kLaneItems == 4, "two additions deep");
+        float sum = (brought(x[0]) + brought(x[1])) + (brought(x[2]) + brought(x[3]));
+        if (S > 32 * kLaneItems) {
+            double rest = sum;
+            for (int i = lane + 32 * kLaneItems; i < S; i += 32) rest += static_cast<double>(brought(__ldcg(&part[w * S + i])));
+            sum = static_cast<float>(rest);
         }
-        __syncthreads();
-        if (!real) bad = 0;  // every thread: what stale partials say is nothing
-        __syncthreads();
-        if (bad) {
-            if (tid < K) {
-                a.out_s[o + tid] = -INFINITY;
-                a.out_p[o + tid] = -1;
-                a.out_t[o + tid] = -1;
-                if (a.out_f) a.out_f[o + tid] = 0;
+        sum = warp_sum(sum);
+        if (lane == 0) {
+            rw.m[w] = top;
+            if (top == -INFINITY) {
+                rw.kind[w] = kRowNone;  // nothing to go on with
+            } else if (!stoch_row_ok(top, sum)) {
+                bad = 1;
+            } else {
+                rw.base[w] = static_cast<double>(rw.score[w]) - log_fast(sum);
+                rw.err[w] = a.err;
+                rw.base32[w] = static_cast<float>(rw.base[w]);
             }
-            if (tid == 0) report(p.status, kStLogit);
-            return;
         }
+        __syncwarp();
+    }
+    __syncthreads();
+    if (bad) {
+        if (tid < K) {
+            a.out_s[o + tid] = -INFINITY;
+            a.out_p[o + tid] = -1;
+            a.out_t[o + tid] = -1;
+            if (a.out_f) a.out_f[o + tid] = 0;
+        }
+        if (tid == 0) report(p.status, kStLogit);
+        return;
+    }
 
-        for (;;) {
-            // a lower bound t0 of the K-th best candidate: the K-th largest of
-            // kGroups maxima of distinct items (each a candidate's score)
-            float mine = -INFINITY;
-            for (int i = tid; i < items; i += kBeamThreads) mine = fmaxf(mine, item_key(i));
-            thread_max[tid] = mine;
-            if (tid == 0) {
-                nlist = 0;
-                ncand = 0;
-                again = 0;
-                bound = 0xFFFFFFFFu;
-            }
-            __syncthreads();
-            // every kGroups-th item to a group: as many groups as items, up to
-            // kGroups, and the best row's best items in different ones
-            if (tid < kGroups) {
+    for (;;) {
+        // a lower bound t0 of the K-th best candidate: the K-th largest of
+        // kGroups maxima of distinct items (each a candidate's score)
+        float mine = -INFINITY;
+        for (int i = tid; i < items; i += kBeamThreads) mine = fmaxf(mine, item_key(i));
+        thread_max[tid] = mine;
+        if (tid == 0) {
+            nlist = 0;
+            ncand = 0;
+            again = 0;
+            bound = 0xFFFFFFFFu;
+        }
+        __syncthreads();
+        // every kGroups-th item to a group: as many groups as items, up to
+        // kGroups, and the best row's best items in different ones
+        if (tid < kGroups) {
 #pragma unroll
-                for (int x = kGroups; x < kBeamThreads; x += kGroups) mine = fmaxf(mine, thread_max[tid + x]);
-                group_max[tid] = mine;
-            }
-            __syncthreads();
-            {
-                // how many of the groups' maxima are larger, four threads a group:
-                // the least of those with fewer than K is the K-th largest
-                constexpr int kShare = kBeamThreads / kGroups;
-                const int j0 = tid % kShare * (kGroups / kShare);
-                const float x = group_max[tid / kShare];
-                int above = 0;
+            for (int x = kGroups; x < kBeamThreads; x += kGroups) mine = fmaxf(mine, thread_max[tid + x]);
+            group_max[tid] = mine;
+        }
+        __syncthreads();
+        {
+            // how many of the groups' maxima are larger, four threads a group:
+            // the least of those with fewer than K is the K-th largest
+            constexpr int kShare = kBeamThreads / kGroups;
+            const int j0 = tid % kShare * (kGroups / kShare);
+            const float x = group_max[tid / kShare];
+            int above = 0;
 #pragma unroll
-                for (int j = j0; j < j0 + kGroups / kShare; j += 4) {
-                    const float4 y = *reinterpret_cast<const float4 *>(&group_max[j]);
-                    above += (y.x > x ? 1 : 0) + (y.y > x ? 1 : 0) + (y.z > x ? 1 : 0) + (y.w > x ? 1 : 0);
-                }
-#pragma unroll
-                for (int o = 1; o < kShare; o <<= 1) above += __shfl_xor_sync(kFull, above, o);
-                const uint32_t least = __reduce_min_sync(kFull, above < K ? order_key(x) : 0xFFFFFFFFu);
-                if (lane == 0) atomicMin(&bound, least);
+            for (int j = j0; j < j0 + kGroups / kShare; j += 4) {
+                const float4 y = *reinterpret_cast<const float4 *>(&group_max[j]);
+                above += (y.x > x ? 1 : 0) + (y.y > x ? 1 : 0) + (y.z > x ? 1 : 0) + (y.w > x ? 1 : 0);
             }
-            __syncthreads();
-            float t0f = order_value(bound);
-            if (t0f <= -FLT_MAX && real) {
-                // fewer than K items (with keys above the lowest): the K-th largest
-                // of the maxima of their parts, 32 bf16 (16 fp32) entries a lane
-                // and half
-                float sub[2] = {-INFINITY, -INFINITY};
-                for (int i = warp; i < items; i += kBeamWarps) {
-                    const int w = row_of(i);
-                    if (rw.kind[w] != kRowLive) continue;
+#pragma unroll
+            for (int o = 1; o < kShare; o <<= 1) above += __shfl_xor_sync(kFull, above, o);
+            const uint32_t least = __reduce_min_sync(kFull, above < K ? order_key(x) : 0xFFFFFFFFu);
+            if (lane == 0) atomicMin(&bound, least);
+        }
+        __syncthreads();
+        float t0f = order_value(bound);
+        if (t0f <= -FLT_MAX) {
+            // fewer than K items (with keys above the lowest): the K-th largest
+            // of the maxima of their parts, 32 bf16 (16 fp32) entries a lane
+            // and half
+            float sub[2] = {-INFINITY, -INFINITY};
+            for (int i = warp; i < items; i += kBeamWarps) {
+                const int w = row_of(i);
+                if (rw.kind[w] != kRowLive) continue;
 #pragma unroll 1
-                    for (int v = 0; v < Pass1Shape<Tag>::kVecL; ++v) {
-                        const float key = key_of(w, vec_max<Tag>(item_vector<Tag>(p, b, w, i - w * S, v)));
-                        if (v < Pass1Shape<Tag>::kVecL / 2) sub[0] = fmaxf(sub[0], key);
-                        else sub[1] = fmaxf(sub[1], key);
-                    }
-                }
-                const uint32_t k0 = order_key(sub[0]), k1 = order_key(sub[1]);
-                uint32_t lo = order_key(-INFINITY), hi = order_key(INFINITY);
-                while (lo < hi) {
-                    const uint32_t mid = lo + (hi - lo + 1) / 2;
-                    if (__syncthreads_count(k0 >= mid) + __syncthreads_count(k1 >= mid) >= K) lo = mid;
-                    else hi = mid - 1;
-                }
-                t0f = order_value(lo);
-            }
-            // the lowest key stands for scores of any size: no bound
-            if (t0f <= -FLT_MAX) t0f = -INFINITY;
-            // below t0 by the rows' errors, so that what the check below
-            // compares is in the list too; and by the keys' rounding, at most
-            // 4 steps of what adds up to a key
-            const double t0 = t0f == -INFINITY ? -INFINITY : static_cast<double>(t0f) - 4.0 * a.err;
-            auto slack = [&](int w) { return 4.8e-7f * (fabsf(t0f) + fabsf(rw.base32[w])); };
-            const float least = t0f == -INFINITY ? -INFINITY : static_cast<float>(t0);
-            for (int i = tid; i < items; i += kBeamThreads) {
-                const float key = item_key(i);
-                if (key > -INFINITY && key >= least - 2.f * slack(row_of(i))) {
-                    const int at = atomicAdd(&nlist, 1);
-                    if (at < kListMax) list[at] = i;
+                for (int v = 0; v < Pass1Shape<Tag>::kVecL; ++v) {
+                    const float key = key_of(w, vec_max<Tag>(item_vector<Tag>(p, b, w, i - w * S, v)));
+                    if (v < Pass1Shape<Tag>::kVecL / 2) sub[0] = fmaxf(sub[0], key);
+                    else sub[1] = fmaxf(sub[1], key);
                 }
             }
-            auto add_done = [&]() {
-                if (tid < W && rw.kind[tid] == kRowDone)
-                    cand[atomicAdd(&ncand, 1)] = {static_cast<double>(rw.score[tid]), tid, a.end_token};
-            };
+            const uint32_t k0 = order_key(sub[0]), k1 = order_key(sub[1]);
+            uint32_t lo = order_key(-INFINITY), hi = order_key(INFINITY);
+            while (lo < hi) {
+                const uint32_t mid = lo + (hi - lo + 1) / 2;
+                if (__syncthreads_count(k0 >= mid) + __syncthreads_count(k1 >= mid) >= K) lo = mid;
+                else hi = mid - 1;
+            }
+            t0f = order_value(lo);
+        }
+        // the lowest key stands for scores of any size: no bound
+        if (t0f <= -FLT_MAX) t0f = -INFINITY;
+        // below t0 by the rows' errors, so that what the check below
+        // compares is in the list too; and by the keys' rounding, at most
+        // 4 steps of what adds up to a key
+        const double t0 = t0f == -INFINITY ? -INFINITY : static_cast<double>(t0f) - 4.0 * a.err;
+        auto slack = [&](int w) { return 4.8e-7f * (fabsf(t0f) + fabsf(rw.base32[w])); };
+        const float least = t0f == -INFINITY ? -INFINITY : static_cast<float>(t0);
+        for (int i = tid; i < items; i += kBeamThreads) {
+            const float key = item_key(i);
+            if (key > -INFINITY && key >= least - 2.f * slack(row_of(i))) {
+                const int at = atomicAdd(&nlist, 1);
+                if (at < kListMax) list[at] = i;
+            }
+        }
+        auto add_done = [&]() {
+            if (tid < W && rw.kind[tid] == kRowDone)
+                cand[atomicAdd(&ncand, 1)] = {static_cast<double>(rw.score[tid]), tid, a.end_token};
+        };
+        add_done();
+        __syncthreads();
+        bool whole = nlist <= kListMax;
+        if (whole) {
+            for (int j = warp; j < nlist; j += kBeamWarps) {
+                const int w = row_of(list[j]);
+                // the row's logits that may reach t0, rounded down
+                float lthr = -INFINITY;
+                if (t0 != -INFINITY) {
+                    const double l = static_cast<double>(rw.m[w]) + (t0 - 2.f * slack(w) - rw.base[w]) / p.inv_t;
+                    lthr = static_cast<float>(l - fabs(l) * 1.2e-7);
+                }
+                gather_item<Tag>(p, b, w, list[j] - w * S, lthr, rw.base[w], rw.m[w], cand, a.cap, &ncand);
+            }
+            __syncthreads();
+            whole = ncand <= a.cap;
+        }
+        if (!whole) {
+            // many equal maxima: exactly the K best items, one by one, and of
+            // each its K best entries (K * K fit the list)
+            int n = 0;
+            Cand last = {INFINITY, -1, -1};
+            __syncthreads();
+            if (tid == 0) ncand = 0;
+            __syncthreads();
             add_done();
-            __syncthreads();
-            bool whole = nlist <= kListMax;
-            if (whole) {
-                for (int j = warp; j < (real ? nlist : min(nlist, kBeamWarps)); j += kBeamWarps) {
-                    const int w = row_of(list[j]);
-                    // the row's logits that may reach t0, rounded down
-                    float lthr = -INFINITY;
-                    if (t0 != -INFINITY) {
-                        const double l = static_cast<double>(rw.m[w]) + (t0 - 2.f * slack(w) - rw.base[w]) / p.inv_t;
-                        lthr = static_cast<float>(l - fabs(l) * 1.2e-7);
-                    }
-                    gather_item<Tag>(p, b, w, list[j] - w * S, lthr, rw.base[w], rw.m[w], cand, a.cap, &ncand);
+            for (; n < K; ++n) {
+                Cand top = {-INFINITY, INT_MAX, INT_MAX};
+                for (int i = tid; i < items; i += kBeamThreads) {
+                    const int w = row_of(i);
+                    const Cand c = {item_score(i), w, i - w * S};
+                    if (c.s > -INFINITY && better(last, c) && better(c, top)) top = c;
                 }
+#pragma unroll
+                for (int x = 16; x > 0; x >>= 1) {
+                    const Cand c = {__shfl_xor_sync(kFull, top.s, x), __shfl_xor_sync(kFull, top.w, x),
+                                    __shfl_xor_sync(kFull, top.v, x)};
+                    if (better(c, top)) top = c;
+                }
+                if (lane == 0) warp_best[warp] = top;
                 __syncthreads();
-                whole = ncand <= a.cap;
-            }
-            if (!whole && real) {
-                // many equal maxima: exactly the K best items, one by one, and of
-                // each its K best entries (K * K fit the list)
-                int n = 0;
-                Cand last = {INFINITY, -1, -1};
+                top = warp_best[0];
+                for (int i = 1; i < kBeamWarps; ++i)
+                    if (better(warp_best[i], top)) top = warp_best[i];
                 __syncthreads();
-                if (tid == 0) ncand = 0;
-                __syncthreads();
-                add_done();
-                for (; n < K; ++n) {
-                    Cand top = {-INFINITY, INT_MAX, INT_MAX};
-                    for (int i = tid; i < items; i += kBeamThreads) {
-                        const int w = row_of(i);
-                        const Cand c = {item_score(i), w, i - w * S};
-                        if (c.s > -INFINITY && better(last, c) && better(c, top)) top = c;
-                    }
-    #pragma unroll
-                    for (int x = 16; x > 0; x >>= 1) {
-                        const Cand c = {__shfl_xor_sync(kFull, top.s, x), __shfl_xor_sync(kFull, top.w, x),
-                                        __shfl_xor_sync(kFull, top.v, x)};
-                        if (better(c, top)) top = c;
-                    }
-                    if (lane == 0) warp_best[warp] = top;
-                    __syncthreads();
-                    top = warp_best[0];
-                    for (int i = 1; i < kBeamWarps; ++i)
-                        if (better(warp_best[i], top)) top = warp_best[i];
-                    __syncthreads();
-                    if (top.s == -INFINITY) break;
-                    if (tid == 0) list[n] = top.w * S + top.v;
-                    last = top;
-                }
-                __syncthreads();
-                for (int j = warp; j < n; j += kBeamWarps) {
-                    const int w = row_of(list[j]);
-                    gather_best<Tag>(p, b, w, list[j] - w * S, rw.base[w], rw.m[w], K, cand, a.cap, &ncand);
-                }
-                if (tid == 0) nlist = n;
+                if (top.s == -INFINITY) break;
+                if (tid == 0) list[n] = top.w * S + top.v;
+                last = top;
             }
             __syncthreads();
-
-            // rank every candidate, a warp each; the first K are the selection
-            const int n = real ? ncand : min(ncand, kBeamWarps);
-            found = min(n, K);
-            for (int i = warp; i < n; i += kBeamWarps) {
-                const Cand c = cand[i];
-                int rank = 0;
-                for (int j = lane; j < n; j += 32) rank += better(cand[j], c) ? 1 : 0;
-                rank = __reduce_add_sync(kFull, rank);
-                if (lane == 0 && rank < K) best[rank] = c;
+            for (int j = warp; j < n; j += kBeamWarps) {
+                const int w = row_of(list[j]);
+                gather_best<Tag>(p, b, w, list[j] - w * S, rw.base[w], rw.m[w], K, cand, a.cap, &ncand);
             }
-            __syncthreads();
-            // rows whose errors could change it
-            auto err = [&](int w) { return rw.kind[w] == kRowLive ? rw.err[w] : 0.0; };
-            auto close = [&](const Cand &x, double s, int w) {
-                const double e = err(x.w) + err(w);
-                return w != x.w && e > 0.0 && fabs(x.s - s) <= e;
-            };
-            auto want = [&](int w) {
-                if (rw.kind[w] == kRowLive && rw.err[w] > 0.0) {
-                    rw.exact[w] = 1;
-                    again = 1;
-                }
-            };
-            if (tid + 1 < found && close(best[tid], best[tid + 1].s, best[tid + 1].w)) {
-                want(best[tid].w);
-                want(best[tid + 1].w);
-            }
-            if (found == K) {
-                const Cand kth = best[K - 1];
-                for (int i = tid; i < n; i += kBeamThreads) {
-                    const Cand c = cand[i];
-                    if (better(kth, c) && close(kth, c.s, c.w)) {
-                        want(kth.w);
-                        want(c.w);
-                    }
-                }
-                // items that are not in the list, by their maxima (a whole list
-                // leaves out only what lies further below)
-                if (!whole && real)
-                    for (int i = tid; i < items; i += kBeamThreads) {
-                        const int w = row_of(i);
-                        const double s = item_score(i);
-                        if (s == -INFINITY || !close(kth, s, w)) continue;
-                        bool in = false;
-                        for (int j = 0; j < nlist && !in; ++j) in = list[j] == i;
-                        if (!in) {
-                            want(kth.w);
-                            want(w);
-                        }
-                    }
-            }
-            __syncthreads();
-            if (!again || !real) break;
-            for (int j = tid; j < kExp2Tab; j += kBeamThreads) tab[j] = p.exp2tab[j];
-            __syncthreads();
-            for (int w = 0; w < W; ++w) {
-                if (rw.exact[w] != 1) continue;
-                const double sum = exact_sum<Tag>(p, b, w, rw.m[w], tab, scratch);
-                if (tid == 0) {
-                    rw.base[w] = static_cast<double>(rw.score[w]) - log(sum);
-                    rw.base32[w] = static_cast<float>(rw.base[w]);
-                    rw.err[w] = 0.0;
-                    rw.exact[w] = 2;
-                }
-            }
-            __syncthreads();
+            if (tid == 0) nlist = n;
         }
+        __syncthreads();
+
+        // rank every candidate, a warp each; the first K are the selection
+        const int n = ncand;
+        found = min(n, K);
+        for (int i = warp; i < n; i += kBeamWarps) {
+            const Cand c = cand[i];
+            int rank = 0;
+            for (int j = lane; j < n; j += 32) rank += better(cand[j], c) ? 1 : 0;
+            rank = __reduce_add_sync(kFull, rank);
+            if (lane == 0 && rank < K) best[rank] = c;
+        }
+        __syncthreads();
+        // rows whose errors could change it
+        auto err = [&](int w) { return rw.kind[w] == kRowLive ? rw.err[w] : 0.0; };
+        auto close = [&](const Cand &x, double s, int w) {
+            const double e = err(x.w) + err(w);
+            return w != x.w && e > 0.0 && fabs(x.s - s) <= e;
+        };
+        auto want = [&](int w) {
+            if (rw.kind[w] == kRowLive && rw.err[w] > 0.0) {
+                rw.exact[w] = 1;
+                again = 1;
+            }
+        };
+        if (tid + 1 < found && close(best[tid], best[tid + 1].s, best[tid + 1].w)) {
+            want(best[tid].w);
+            want(best[tid + 1].w);
+        }
+        if (found == K) {
+            const Cand kth = best[K - 1];
+            for (int i = tid; i < n; i += kBeamThreads) {
+                const Cand c = cand[i];
+                if (better(kth, c) && close(kth, c.s, c.w)) {
+                    want(kth.w);
+                    want(c.w);
+                }
+            }
+            // items that are not in the list, by their maxima (a whole list
+            // leaves out only what lies further below)
+            if (!whole)
+                for (int i = tid; i < items; i += kBeamThreads) {
+                    const int w = row_of(i);
+                    const double s = item_score(i);
+                    if (s == -INFINITY || !close(kth, s, w)) continue;
+                    bool in = false;
+                    for (int j = 0; j < nlist && !in; ++j) in = list[j] == i;
+                    if (!in) {
+                        want(kth.w);
+                        want(w);
+                    }
+                }
+        }
+        __syncthreads();
+        if (!again) break;
+        for (int j = tid; j < kExp2Tab; j += kBeamThreads) tab[j] = p.exp2tab[j];
+        __syncthreads();
+        for (int w = 0; w < W; ++w) {
+            if (rw.exact[w] != 1) continue;
+            const double sum = exact_sum<Tag>(p, b, w, rw.m[w], tab, scratch);
+            if (tid == 0) {
+                rw.base[w] = static_cast<double>(rw.score[w]) - log(sum);
+                rw.base32[w] = static_cast<float>(rw.base[w]);
+                rw.err[w] = 0.0;
+                rw.exact[w] = 2;
+            }
+        }
+        __syncthreads();
     }
     if (tid < K) {
         const bool in = tid < found;

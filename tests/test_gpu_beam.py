@@ -330,3 +330,15 @@ def test_more_requests_than_start_together(sv, dtype, B, W, K, V):
     s[B - 2, 0] = float("nan")
     _, p, _ = check(sv, x, s, V, K, 0.8, fin, 3)
     assert np.all(p[B - 2] == -1) and np.any(p[148:] >= 0)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_what_the_workspace_held_changes_nothing(sv, dtype):
+    x, s = rows(23, 5, 4, 9001, dtype)
+    x, s = x.cuda(), s.cuda()
+    want = sv.spec_beam_select(x, s, 9001, 6)
+    need = sv.load_library().spec_beam_workspace_size(5, 4, 9001)
+    for fill in (0, 63, 127, 255):
+        ws = torch.full((need,), fill, dtype=torch.uint8, device="cuda")
+        got = sv.spec_beam_select(x, s, 9001, 6, workspace_buf=ws)
+        assert all(torch.equal(a, b) for a, b in zip(got[:3], want[:3]))

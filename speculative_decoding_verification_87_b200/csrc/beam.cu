@@ -378,8 +378,9 @@ __device__ __forceinline__ double exact_sum(const Params &p, int b, int w, float
 // Select: one block per request, after pass 1.  A chain of block-wide steps
 // bounds it, not bytes: 6 us after pass 1's end for one request with K = 4, 9
 // for 32 with K = 16.  Where rows' sums are recomputed each of 128256 entries
-// takes some 20 us more, one after the other: equal beams, which are all
-// recomputed, take 97 us for 4 and 1.34 ms for 64 (12 and 36 for distinct ones).
+// takes some 20 us more, one after the other: a call with 4 equal beams, which
+// are all recomputed, takes 100 us, one with 64 1.4 ms (distinct beams 9 us, and
+// 30 to 90 as near ties come).
 template <class Tag>
 __global__ void __launch_bounds__(kBeamThreads)
     k_beam_select(const __grid_constant__ BeamParams p, const __grid_constant__ BeamArgs a)
@@ -762,8 +763,8 @@ int launch_beam(BeamParams &p, BeamArgs &a, int dtype_index, cudaStream_t st)
         std::max<int64_t>(1, std::min<int64_t>(static_cast<int64_t>(per_sm) * sms, ceil_div(p.nA, kWarps)));
     // All items are static: the claimed tail of the other calls comes in
     // chunks of four items and clearing its counter is a launch of its own
-    // (rows of 128256 bf16: 32 x 16 42.7 us static, 48.7 with a claimed tail;
-    // 128 x 16 139.5 and 143.1; 256 x 4 65.8 and 70.5)
+    // (rows of 128256 bf16: a claimed tail takes 6.0 us more for 32 x 16, 3.6 for
+    // 128 x 16, 4.7 for 256 x 4)
     p.nAs = p.nA;
     k_beam_pass1<Tag><<<static_cast<unsigned>(blocks), kThreads, kRingBytes, st>>>(p);
     if (cudaGetLastError() != cudaSuccess) return SPEC_ECUDA;

@@ -949,12 +949,15 @@ size_t align_up(size_t x) { return (x + kScoreAlign - 1) / kScoreAlign * kScoreA
 std::mutex g_score_mu;
 // Few rows, for the form that stores its products: while that moves no more
 // (8 bytes a product, there and back) than a second read of the keys.  (bf16,
-// half a million slots, stored / swept twice: R = 16, D = 128 40 / 67 us; R =
-// 32, D = 128 57 / 73; R = 16, D = 64 28 / 37; R = 32, D = 64 46 / 45.)  Below
-// a quarter million bf16 slots the keys' second read comes from L2 and only
-// half as many rows pay (64 K slots, D = 128: R = 8 11.7 / 13.8 us, R = 16
-// 15.8 / 13.9, R = 24 21.0 / 15.4).  In fp32 the products cost six times as
-// much and are not formed twice (128 K slots: R = 32, D = 128 45 / 85 us).
+// stored / swept twice, us.  512 K slots in 32 heads, D = 64, 128, 256: R = 16
+// 26 / 36, 34 / 63, 70 / 152; R = 32 36 / 44, 46 / 68, 83 / 135.)  The second
+// kernel merges every chunk's statistics in each of its blocks, which tells with
+// rows and with long heads where the slots are few: below a quarter million
+// half as many rows pay.  (64 K slots, R = 16: D = 64 9.9 / 10.6 in 32 heads, 12.1 /
+// 10.5 in 8, 17.2 / 11.8 in one; D = 128 11.0 / 13.7, 13.1 / 14.2, 18.1 / 15.3.  R =
+// 32, D = 128: 14.9 / 15.9, 18.7 / 15.6, 23.9 / 16.9; D = 256 22.4 / 25.1, 26.5 /
+// 25.1, 31.3 / 26.4.)  In fp32 the products cost six times as much and are not
+// formed twice (128 K slots: R = 32, D = 128 45 / 85 us).
 bool few_rows(bool f32, int R, int D, int64_t slots)
 {
     if (f32) return R <= kFewRows && 2 * R <= D;

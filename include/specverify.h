@@ -429,9 +429,9 @@ SPECVERIFY_API int spec_commit_path(void *const *states, int num_states, int64_t
  * 0 <= begin <= end <= capacity and end - begin <= Q, else the request is
  * left as it was and SPEC_STATUS_CAPACITY set.  A query whose products hold a
  * NaN or +inf gives NaN weights to the slots it sees.  A product of -inf weighs
- * nothing, and a query that has no other adds nothing.  8 <= D <= SPEC_MAX_HEAD_DIM, a multiple of
- * 16 bytes; Q * G and B * kv_heads at most 65535, capacity at most 2^30;
- * scale * log2(e) finite in fp32.
+ * nothing, and a query that has no other adds nothing.  8 <= D <=
+ * SPEC_MAX_HEAD_DIM, a multiple of 16 bytes; Q * G and B * kv_heads at most
+ * 65535, capacity at most 2^30; scale * log2(e) finite in fp32.
  * workspace: at least spec_score_workspace_size_for(...) bytes of the call's
  * type and head dimension, 256-byte aligned, not shared by calls that may
  * overlap.  While a key head's rows Q * G are few (up to 32, and to a fraction

@@ -15,7 +15,7 @@
 // request, whatever W is.
 //
 // Order.  The scores are compared as exact numbers.  Pass 1 leaves base_w
-// with an error below kBaseErr (BeamArgs::err); two candidates of different rows that lie
+// with an error below BeamArgs::err; two candidates of different rows that lie
 // within the sum of their rows' errors are told apart by recomputing those
 // rows' sums in fp64 (one block, rarely: with K = 16 about one request in a
 // thousand), after which the order holds to fp64 rounding.
@@ -433,10 +433,10 @@ __global__ void __launch_bounds__(kBeamThreads)
     };
     const int64_t o = static_cast<int64_t>(b) * K;
     int found = 0;
-    // (Running the steps once on the last call's partials while pass 1 streams, to
-    // have their instructions at hand, took 2.7 us more of 8.8: blocks start when
-    // the first of pass 1 leave, so the first run is waited for too; on partials of
-    // other contents 10 us more.)
+    // (Running the steps once before this, on the workspace's old contents, to have
+    // their instructions at hand, took 2.7 us more than the 8.8 of one request: the
+    // block starts when the first of pass 1 leave, so that run is waited for too.
+    // On contents other than a last call's partials it took 10 us more.)
     asm volatile("griddepcontrol.wait;\n" ::: "memory");
     __syncthreads();
     // merge the rows, a warp each
@@ -857,6 +857,7 @@ extern "C" int spec_beam_select(const void *logits, spec_dtype_t dtype, int64_t 
     p.rowpart = reinterpret_cast<float2 *>(static_cast<char *>(workspace) + kBeamAlign);
     static const Exp2Table table;  // 2 us of a call that takes 15
     std::memcpy(p.exp2tab, table.at, sizeof p.exp2tab);
-    BeamArgs a{end_token, keep, 0, vocab <= kLongRow ? kBaseErr : kBaseErrLong, out_scores, out_parents, out_tokens, out_finished};
+    BeamArgs a{end_token,  keep,        0,          vocab <= kLongRow ? kBaseErr : kBaseErrLong,
+               out_scores, out_parents, out_tokens, out_finished};
     return dtype == SPEC_BF16 ? launch_beam<Bf16>(p, a, 1, stream) : launch_beam<F32>(p, a, 0, stream);
 }
